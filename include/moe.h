@@ -62,8 +62,8 @@ typedef enum {
     MOE_ERR_WORKSPACE = 3,    /* workspace missing or smaller than moe_workspace_size */
     MOE_ERR_CUDA = 4,         /* a CUDA call or kernel launch failed */
     MOE_ERR_TIMEOUT = 5,      /* a bounded device wait gave up (see moe_check_device_status) */
-    MOE_ERR_RANGE = 6         /* a device-side bounds check refused a row (inconsistent counts;
-                                 see moe_check_device_status and the expert-parallel calls) */
+    MOE_ERR_RANGE = 6         /* a device-side bounds check refused a row (inconsistent counts or offsets;
+                                 see moe_check_device_status, the expert-parallel and the grouped calls) */
 } moe_status_t;
 
 typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1 } moe_dtype_t;
@@ -301,6 +301,73 @@ moe_status_t moe_dispatch_noalloc(const moe_config_t* cfg, const void* x, const 
 moe_status_t moe_expert_ffn(const moe_config_t* cfg, const moe_weights_t* weights, const void* x_perm,
                             const int32_t* offsets, void* y_perm, void* ws, size_t ws_bytes,
                             cudaStream_t stream);
+
+/* ---- Grouped products over sorted rows, and their gradients ------------
+ * The matrix products of the experts as calls of their own, for training and
+ * for expert forms that moe_expert_ffn does not have: rows
+ * [offsets[e], offsets[e+1]) of the row buffers belong to expert e.
+ *   moe_grouped_gemm         y[r]  = x[r] W[e] (+ bias[e])
+ *   moe_grouped_gemm_grad_x  dx[r] = dy[r] W[e]^T
+ *   moe_grouped_gemm_grad_w  dW[e] = x_e^T dy_e,  db[e] = sum of the rows dy_e
+ * with x, dx [rows, K]; y, dy [rows, N]; w, dw [E, K, N]; bias, db [E, N].
+ * Rows from offsets[E] on are neither read for a result nor written, whatever
+ * they hold (NaN included), and no expert's values reach another's.  An expert
+ * without rows gets dW = 0, db = 0 (unchanged when accumulating).
+ * bf16: tensor cores, fp32 accumulation, one rounding of each output; K and N
+ * multiples of 8.  f32: fp32 FMA; K and N multiples of 4.  offsets (DEVICE
+ * [E+1] int32) are checked on the device: an expert whose offsets decrease or
+ * leave [0, rows] is taken as empty and MOE_ERR_RANGE recorded.
+ * Limits: 1 <= E <= 64; 0 <= rows < 2^31 - 1024.  The workspace holds
+ * moe_grouped_workspace_size bytes (moe_workspace_init once). */
+typedef struct {
+    int64_t rows;   /* rows of the row buffers (offsets[E] at most) */
+    int32_t E;      /* experts */
+    int32_t K;      /* columns of x: rows of each expert's matrix */
+    int32_t N;      /* columns of y: columns of each expert's matrix */
+    int32_t dtype;  /* moe_dtype_t of x, y, dy, dx, w and bias */
+} moe_grouped_config_t;
+
+moe_status_t moe_grouped_workspace_size(const moe_grouped_config_t* cfg, size_t* bytes);
+/* bias [E, N] or NULL. */
+moe_status_t moe_grouped_gemm(const moe_grouped_config_t* cfg, const void* x, const void* w, const void* bias,
+                              const int32_t* offsets, void* y, void* ws, size_t ws_bytes, cudaStream_t stream);
+moe_status_t moe_grouped_gemm_grad_x(const moe_grouped_config_t* cfg, const void* dy, const void* w,
+                                     const int32_t* offsets, void* dx, void* ws, size_t ws_bytes,
+                                     cudaStream_t stream);
+/* grad_dtype: moe_dtype_t of dw and db, MOE_DT_F32 or the config's dtype.
+ * db [E, N] or NULL.  accumulate != 0: dw and db are added to (in fp32, with
+ * one rounding), as over micro-batches. */
+moe_status_t moe_grouped_gemm_grad_w(const moe_grouped_config_t* cfg, const void* x, const void* dy,
+                                     const int32_t* offsets, void* dw, void* db, int32_t grad_dtype,
+                                     int32_t accumulate, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Gradients of moe_expert_ffn (SwiGLU: W_down(silu(x W_gate) * x W_up); GELU:
+ * W2 gelu(x W1 + b1) + b2), layouts as the weights'.  A NULL pointer leaves
+ * that gradient out. */
+typedef struct {
+    void* dx;             /* [R_max, d] config dtype, rows < offsets[E] written */
+    void* w_gate_or_w1;   /* [E, d, ffn] */
+    void* w_up;           /* [E, d, ffn]  SwiGLU only */
+    void* w_down_or_w2;   /* [E, ffn, d] */
+    void* b1;             /* [E, ffn] GELU only */
+    void* b2;             /* [E, d]   GELU only */
+    int32_t grad_dtype;   /* moe_dtype_t of the weights' and biases' gradients: MOE_DT_F32 or the config's */
+    int32_t accumulate;   /* != 0: the weights' and biases' gradients are added to; dx is always written */
+} moe_ffn_grads_t;
+
+/* Backward pass of moe_expert_ffn: from x_perm [R_max, d], offsets [E+1] and
+ * the gradient dy_perm [R_max, d] of y_perm to `grads`.  Nothing is kept from
+ * the forward pass: the inner activations are formed again from x_perm, in
+ * fp32, inside the product that needs them, and rounded to the dtype once
+ * where the next product reads them; the gradient of the inner activation is
+ * kept in fp32.  dy_perm is the gradient of the unweighted expert outputs (a
+ * weighted combine hands down topk_w[t,j] * dout[t]).  Native weights only;
+ * shared experts are expert FFNs of one group and take a config of E = k = 1.
+ * The workspace holds moe_expert_ffn_backward_workspace_size bytes. */
+moe_status_t moe_expert_ffn_backward_workspace_size(const moe_config_t* cfg, size_t* bytes);
+moe_status_t moe_expert_ffn_backward(const moe_config_t* cfg, const moe_weights_t* weights, const void* x_perm,
+                                     const int32_t* offsets, const void* dy_perm, const moe_ffn_grads_t* grads,
+                                     void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /* Weighted combine back to token order (LLaMA4-MoE §2.4; MoE-basics §3.1):
  * out[t] = sum over j with slot[t,j] >= 0 of topk_w[t,j] * y_perm[slot[t,j]],

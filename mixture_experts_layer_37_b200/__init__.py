@@ -117,7 +117,9 @@ EXPORTED_SYMBOLS = ("moe_status_string", "moe_capacity", "moe_max_rows", "moe_wo
                     "moe_dp_finish", "moe_pipeline_create", "moe_pipeline_submit", "moe_pipeline_wait",
                     "moe_pipeline_check", "moe_pipeline_destroy", "moe_quantize_int8", "moe_ep_recv_rows",
                     "moe_ep_workspace_size", "moe_ep_route", "moe_ep_dispatch", "moe_ep_expert_ffn",
-                    "moe_ep_combine", "moe_ipc_export", "moe_ipc_open", "moe_ipc_close")
+                    "moe_ep_combine", "moe_ipc_export", "moe_ipc_open", "moe_ipc_close",
+                    "moe_grouped_workspace_size", "moe_grouped_gemm", "moe_grouped_gemm_grad_x",
+                    "moe_grouped_gemm_grad_w", "moe_expert_ffn_backward_workspace_size", "moe_expert_ffn_backward")
 
 
 # ---------------------------------------------------------------- config
@@ -638,3 +640,147 @@ def quantize_expert_weights(cfg: MoEConfig, weights: dict, stream=None) -> dict:
         out[name] = q
         out[name + "_scale"] = s
     return out
+
+
+# ---------------------------------------------------------------- grouped products and the FFN's backward pass
+class MoEGroupedConfigC(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("E", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class MoEFfnGradsC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dx", "w_gate_or_w1", "w_up", "w_down_or_w2", "b1", "b2")] + \
+        [("grad_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
+
+
+@dataclass(frozen=True)
+class GroupedConfig:
+    """Sizes of a grouped product: rows of the row buffers, experts, and each
+    expert's [K, N] matrix."""
+    rows: int
+    E: int
+    K: int
+    N: int
+    dtype: str = "bf16"        # "bf16" | "f32"
+
+    def c(self) -> MoEGroupedConfigC:
+        return MoEGroupedConfigC(self.rows, self.E, self.K, self.N, MOE_DT_BF16 if self.dtype == "bf16" else MOE_DT_F32)
+
+    @property
+    def torch_dtype(self) -> torch.dtype:
+        return torch.bfloat16 if self.dtype == "bf16" else torch.float32
+
+
+_GCFG = ctypes.POINTER(MoEGroupedConfigC)
+_fns: dict = {}
+
+
+def _fn(name: str, *argtypes):
+    """The library's function `name`, declared once."""
+    f = _fns.get(name)
+    if f is None:
+        f = getattr(lib(), name)
+        f.argtypes = list(argtypes)
+        f.restype = ctypes.c_int
+        _fns[name] = f
+    return f
+
+
+def _expect(where: str, device, *specs) -> None:
+    """Each (tensor or None, shape, dtypes): a contiguous tensor on `device`."""
+    for t, shape, dtypes in specs:
+        if t is None:
+            continue
+        if tuple(t.shape) != shape or t.dtype not in dtypes or not t.is_contiguous() or t.device != device:
+            raise MoEError(MOE_ERR_INVALID_ARG, f"{where}: a contiguous tensor {list(shape)} of {dtypes} on {device} "
+                                                f"is wanted, got {list(t.shape)} {t.dtype} on {t.device}")
+
+
+def _call_on(device, name: str, f, args, stream) -> None:
+    """f(*args, stream) with `device` current (its current stream where none is given)."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        _check(f(*args, _stream(stream)), name)
+    else:
+        with torch.cuda.device(device):
+            _check(f(*args, _stream(stream)), name)
+
+
+def _dtype_code(dtype: torch.dtype) -> int:
+    return MOE_DT_BF16 if dtype == torch.bfloat16 else MOE_DT_F32
+
+
+def moe_grouped_workspace_size(g: GroupedConfig) -> int:
+    v = ctypes.c_size_t()
+    f = _fn("moe_grouped_workspace_size", _GCFG, ctypes.POINTER(ctypes.c_size_t))
+    _check(f(ctypes.byref(g.c()), ctypes.byref(v)), "moe_grouped_workspace_size")
+    return v.value
+
+
+def moe_grouped_gemm(g: GroupedConfig, x, w, offsets, y, ws: Workspace, bias=None, stream=None) -> None:
+    """y[r] = x[r] w[e] (+ bias[e]) for the rows r in [offsets[e], offsets[e+1])."""
+    dt = (g.torch_dtype,)
+    _expect("moe_grouped_gemm", w.device, (x, (g.rows, g.K), dt), (w, (g.E, g.K, g.N), dt), (y, (g.rows, g.N), dt),
+            (bias, (g.E, g.N), dt), (offsets, (g.E + 1,), (torch.int32,)))
+    f = _fn("moe_grouped_gemm", _GCFG, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P)
+    _call_on(w.device, "moe_grouped_gemm", f, (ctypes.byref(g.c()), _ptr(x), _ptr(w), _ptr(bias), _ptr(offsets),
+                                               _ptr(y), ws.ptr, ws.nbytes), stream)
+
+
+def moe_grouped_gemm_grad_x(g: GroupedConfig, dy, w, offsets, dx, ws: Workspace, stream=None) -> None:
+    """dx[r] = dy[r] w[e]^T for the rows r in [offsets[e], offsets[e+1])."""
+    dt = (g.torch_dtype,)
+    _expect("moe_grouped_gemm_grad_x", w.device, (dy, (g.rows, g.N), dt), (w, (g.E, g.K, g.N), dt),
+            (dx, (g.rows, g.K), dt), (offsets, (g.E + 1,), (torch.int32,)))
+    f = _fn("moe_grouped_gemm_grad_x", _GCFG, _P, _P, _P, _P, _P, ctypes.c_size_t, _P)
+    _call_on(w.device, "moe_grouped_gemm_grad_x", f, (ctypes.byref(g.c()), _ptr(dy), _ptr(w), _ptr(offsets), _ptr(dx),
+                                                      ws.ptr, ws.nbytes), stream)
+
+
+def moe_grouped_gemm_grad_w(g: GroupedConfig, x, dy, offsets, dw, ws: Workspace, db=None, accumulate: bool = False,
+                            stream=None) -> None:
+    """dw[e] = x_e^T dy_e and db[e] = sum of dy_e over the rows of e, added to
+    what is there with `accumulate`; dw and db in g's dtype or float32."""
+    dt, gdt = (g.torch_dtype,), {g.torch_dtype, torch.float32}
+    _expect("moe_grouped_gemm_grad_w", dw.device, (x, (g.rows, g.K), dt), (dy, (g.rows, g.N), dt),
+            (dw, (g.E, g.K, g.N), gdt), (db, (g.E, g.N), (dw.dtype,)), (offsets, (g.E + 1,), (torch.int32,)))
+    f = _fn("moe_grouped_gemm_grad_w", _GCFG, _P, _P, _P, _P, _P, ctypes.c_int32, ctypes.c_int32, _P, ctypes.c_size_t,
+            _P)
+    _call_on(dw.device, "moe_grouped_gemm_grad_w", f,
+             (ctypes.byref(g.c()), _ptr(x), _ptr(dy), _ptr(offsets), _ptr(dw), _ptr(db), _dtype_code(dw.dtype),
+              1 if accumulate else 0, ws.ptr, ws.nbytes), stream)
+
+
+def moe_expert_ffn_backward_workspace_size(cfg: MoEConfig) -> int:
+    v = ctypes.c_size_t()
+    f = _fn("moe_expert_ffn_backward_workspace_size", _CFG, ctypes.POINTER(ctypes.c_size_t))
+    _check(f(ctypes.byref(cfg.c()), ctypes.byref(v)), "moe_expert_ffn_backward_workspace_size")
+    return v.value
+
+
+def moe_expert_ffn_backward(cfg: MoEConfig, weights: dict, x_perm, offsets, dy_perm, grads: dict, ws: Workspace,
+                            accumulate: bool = False, stream=None) -> None:
+    """Gradients of moe_expert_ffn.  grads: "dx" [R_max, d] and, by the weights'
+    names, w_gate / w_up / w_down or w1 / b1 / w2 / b2, each like its weight in
+    the config's dtype or all in float32; a missing one is left out."""
+    R, E, d, n = moe_max_rows(cfg), cfg.E, cfg.d, cfg.ffn
+    dt = (cfg.torch_dtype,)
+    shapes = {"w_gate": (E, d, n), "w_up": (E, d, n), "w_down": (E, n, d)} if cfg.act == "swiglu" else \
+        {"w1": (E, d, n), "b1": (E, n), "w2": (E, n, d), "b2": (E, d)}
+    unknown = set(grads) - set(shapes) - {"dx"}
+    if unknown:
+        raise MoEError(MOE_ERR_INVALID_ARG, f"moe_expert_ffn_backward: no gradients {sorted(unknown)} of {cfg.act}")
+    given = [grads[k] for k in shapes if grads.get(k) is not None]
+    gdt = (given[0].dtype,) if given and given[0].dtype in (cfg.torch_dtype, torch.float32) else dt
+    dev = x_perm.device
+    _expect("moe_expert_ffn_backward", dev, (x_perm, (R, d), dt), (dy_perm, (R, d), dt), (grads.get("dx"), (R, d), dt),
+            (offsets, (E + 1,), (torch.int32,)), *((weights.get(k), s, dt) for k, s in shapes.items()),
+            *((grads.get(k), s, gdt) for k, s in shapes.items()))
+    g = lambda *names: _ptr(next((grads[k] for k in names if grads.get(k) is not None), None))  # noqa: E731
+    gc = MoEFfnGradsC(g("dx"), g("w_gate", "w1"), g("w_up"), g("w_down", "w2"), g("b1"), g("b2"), _dtype_code(gdt[0]),
+                      1 if accumulate else 0)
+    wc = _weights_c(weights)
+    f = _fn("moe_expert_ffn_backward", _CFG, ctypes.POINTER(MoEWeightsC), _P, _P, _P, ctypes.POINTER(MoEFfnGradsC), _P,
+            ctypes.c_size_t, _P)
+    _call_on(dev, "moe_expert_ffn_backward", f,
+             (ctypes.byref(cfg.c()), ctypes.byref(wc), _ptr(x_perm), _ptr(offsets), _ptr(dy_perm), ctypes.byref(gc),
+              ws.ptr, ws.nbytes), stream)

@@ -176,7 +176,10 @@ __device__ __forceinline__ void epilogue_rows(const GemmParams& p, uint32_t tbas
 // box [box_outer, box_inner], 128-byte swizzle, zero fill out of bounds.
 bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch, uint32_t box_inner,
               uint32_t box_outer);
-// The same for any element type, without swizzle (rows land in shared memory as they are in memory).
+// 3-D bf16 tensor [outer, mid, inner] (contiguous), box [1, box_mid, box_inner], 128-byte swizzle, zero fill.
+bool make_map_3d(CUtensorMap* m, const void* base, int64_t outer, int64_t mid, int64_t inner, uint32_t box_inner,
+                 uint32_t box_mid);
+// The same as make_map for any element type, without swizzle (rows land in shared memory as they are in memory).
 bool make_map_plain(CUtensorMap* m, CUtensorMapDataType dtype, const void* base, uint64_t inner, uint64_t outer,
                     uint64_t pitch, uint32_t box_inner, uint32_t box_outer);
 

@@ -1,0 +1,119 @@
+// Launch interfaces of the grouped products and their gradients.  Internal to
+// libmoe.
+#pragma once
+
+#include "internal.h"
+
+namespace moe {
+
+// Which tiles belong to which expert, built by every CTA in shared memory from
+// the offsets on the device (the host never reads the routing).
+struct GroupTables {
+    int start[kMaxExperts + 1];  // first row tile (or, of the weight gradients, output tile) of the i-th expert taken
+    int row0[kMaxExperts];       // its first row
+    int nrows[kMaxExperts];      // its rows
+    int expert[kMaxExperts];     // which expert it is
+};
+
+#ifdef __CUDACC__
+// The rows of expert e.  Offsets that decrease or leave the buffers are
+// refused: such an expert has no rows, and the status word says so.
+__device__ __forceinline__ void group_rows(const int32_t* offsets, int rows, int e, const DevStatus& st, int& row0,
+                                           int& n) {
+    const int a = offsets[e], b = offsets[e + 1];
+    const bool ok = a >= 0 && b >= a && b <= rows;
+    if (!ok) report_range(st, SITE_GROUPED_OFFSETS);
+    row0 = ok ? a : 0;
+    n = ok ? b - a : 0;
+}
+
+// One warp; each lane holds experts `lane` and `lane + 32`.  BY_ROWS: experts
+// in order of falling row count (ties: lower id) with m_tiles tiles each; else
+// in their own order with one tile per bm rows.
+template <bool BY_ROWS>
+__device__ __forceinline__ void build_group_tables(const int32_t* offsets, int rows, int E, int bm, int m_tiles,
+                                                   const DevStatus& st, GroupTables* t, int lane) {
+    int o[2] = {0, 0}, n[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (lane + 32 * i < E) group_rows(offsets, rows, lane + 32 * i, st, o[i], n[i]);
+    int rank[2] = {lane, lane + 32};
+    if (BY_ROWS) {
+        rank[0] = rank[1] = 0;
+        for (int j = 0; j < E; ++j) {
+            const int nj = __shfl_sync(0xffffffffu, j < 32 ? n[0] : n[1], j & 31);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (nj > n[i] || (nj == n[i] && j < lane + 32 * i)) ++rank[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (lane + 32 * i < E) {
+            t->row0[rank[i]] = o[i];
+            t->nrows[rank[i]] = n[i];
+            t->expert[rank[i]] = lane + 32 * i;
+        }
+    if (BY_ROWS) {
+        for (int e = lane; e <= E; e += 32) t->start[e] = e * m_tiles;
+    } else {
+        int carry = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int v = (n[i] + bm - 1) / bm;
+            int s = v;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, s, d);
+                if (lane >= d) s += u;
+            }
+            if (lane + 32 * i < E) t->start[lane + 32 * i] = carry + s - v;
+            carry += __shfl_sync(0xffffffffu, s, 31);
+        }
+        if (lane == 0) t->start[E] = carry;
+    }
+    __syncwarp();
+}
+#endif
+
+enum { GRAD_NONE = 0, GRAD_SWIGLU = 1, GRAD_GELU = 2 };
+
+// Weights w [E, K, N]; x [rows, K]; dy [rows, N] (see grouped_gemm.cu).
+struct GroupedArgs {
+    const int32_t* offsets = nullptr;  // [E+1]
+    int64_t rows = 0;                  // rows of the row buffers
+    int E = 0, K = 0, N = 0;
+    const void* x = nullptr;
+    const void* w = nullptr;
+    const void* bias = nullptr;        // [E, N] or null
+    void* y = nullptr;                 // [rows, N]
+    const void* dy = nullptr;
+    void* dx = nullptr;                // [rows, K]
+    void* dw = nullptr;                // [E, K, N]
+    void* db = nullptr;                // [E, N] or null
+    bool out_f32 = false;              // GX, GW: fp32 output
+    bool accumulate = false;           // GW: dw += , db +=
+    // GX with a second pair: dx = dy w^T + dy2 w2^T
+    const void* dy2 = nullptr;
+    const void* w2 = nullptr;          // also: the up matrix of GRAD_SWIGLU
+    // FWD with the activation's backward pass in its epilogue (y is not written)
+    int grad_act = GRAD_NONE;
+    const void* dh = nullptr;          // [rows, N] fp32
+    void* h = nullptr;                 // [rows, N] activation
+    void* d0 = nullptr;                // [rows, N] gradient of gate (SwiGLU) or of the pre-activation (GELU)
+    void* d1 = nullptr;                // [rows, N] gradient of up (SwiGLU)
+    DevStatus st;
+};
+
+cudaError_t launch_grouped_fwd_bf16(const GroupedArgs& a, cudaStream_t s);
+cudaError_t launch_grouped_gx_bf16(const GroupedArgs& a, cudaStream_t s);
+cudaError_t launch_grouped_gw_bf16(const GroupedArgs& a, cudaStream_t s);
+cudaError_t launch_grouped_fwd_f32(const GroupedArgs& a, cudaStream_t s);
+cudaError_t launch_grouped_gx_f32(const GroupedArgs& a, cudaStream_t s);
+cudaError_t launch_grouped_gw_f32(const GroupedArgs& a, cudaStream_t s);
+// db[e,n] (+)= sum over the rows of e of dy[r,n]; db in fp32 (a.out_f32) or bf16.
+cudaError_t launch_grouped_colsum(const GroupedArgs& a, bool dy_bf16, cudaStream_t s);
+// Elementwise over all rows in fp32: from g, u and dh to h (over dh), dg (over g), du (over u).
+cudaError_t launch_act_grad_f32(int act, int64_t n, float* g, float* u, float* dh, cudaStream_t s);
+
+}  // namespace moe

@@ -1,0 +1,366 @@
+// Grouped matrix products over rows sorted by expert and their gradients in
+// fp32 FMA (no TF32): the precision-reference path of float32 configurations,
+// and two small kernels of the backward pass (bias gradients; the expert
+// activation's gradient on fp32 buffers).  The three forms are those of
+// grouped_gemm.cu.
+//
+// One CTA per output tile, 256 threads, each TM/16 x TN/16 outputs; operands
+// staged 16 deep through shared memory, the next 16 loaded into registers
+// while the current ones are used; the FMAs run two at a time (f32x2, each
+// rounded as a scalar fmaf).  Every output is one sum in ascending order of
+// the contraction.  Rows and columns outside the expert are never read.
+#include <math.h>
+
+#include "grouped.h"
+
+namespace moe {
+namespace {
+
+constexpr int TK = 16;
+constexpr int kF32Threads = 256;
+
+enum { FORM_FWD = 0, FORM_GX = 1, FORM_GW = 2 };
+
+struct F32Params {
+    const float* A = nullptr;   // FWD: x [rows, K]; GX: dy [rows, N]; GW: x
+    const float* B = nullptr;   // FWD, GX: w [E, K, N]; GW: dy
+    const float* bias = nullptr;
+    float* out = nullptr;
+    const int32_t* offsets = nullptr;
+    int rows = 0, E = 0, K = 0, N = 0, n_tiles = 0, m_tiles = 0;
+    int accumulate = 0;
+    DevStatus st;
+};
+
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// One operand's [TK x T] piece: PER float4 per thread, from memory that is
+// contiguous along the tile (KC = false) or along the contraction (KC = true).
+// base points at tile element 0, contraction element 0; ld is the stride of
+// the other axis; t_n, k_n say how many of each exist from here.
+template <int T, bool KC>
+struct Piece {
+    static constexpr int PER = T * TK / 4 / kF32Threads > 0 ? T * TK / 4 / kF32Threads : 1;
+    static constexpr bool kAll = T * TK / 4 >= kF32Threads;
+    float4 v[PER];
+    __device__ __forceinline__ void load(const float* base, int64_t ld, int t_n, int k0, int k_n) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int id = threadIdx.x + i * kF32Threads;
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (!kAll && id >= T * TK / 4) continue;
+            const int k = k0 + (KC ? id % (TK / 4) * 4 : id / (T / 4));
+            const int t = KC ? id / (TK / 4) : id % (T / 4) * 4;
+            if (k < k_n && t < t_n)
+                v[i] = *reinterpret_cast<const float4*>(base + (KC ? t * ld + k : k * ld + t));
+        }
+    }
+    __device__ __forceinline__ void store(float (*s)[T + 4]) const {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int id = threadIdx.x + i * kF32Threads;
+            if (!kAll && id >= T * TK / 4) continue;
+            if (KC) {
+                const int k = id % (TK / 4) * 4, t = id / (TK / 4);
+                s[k][t] = v[i].x;
+                s[k + 1][t] = v[i].y;
+                s[k + 2][t] = v[i].z;
+                s[k + 3][t] = v[i].w;
+            } else {
+                *reinterpret_cast<float4*>(&s[id / (T / 4)][id % (T / 4) * 4]) = v[i];
+            }
+        }
+    }
+};
+
+// A thread's outputs: rows ty*RM + 64*i.. in groups of at most 4, columns the same.
+template <int FORM, int TM, int TN>
+__global__ void __launch_bounds__(kF32Threads) grouped_f32_kernel(F32Params p) {
+    constexpr int RM = TM / 16, RN = TN / 16;          // outputs per thread: RM rows, RN columns
+    constexpr int GM = RM < 4 ? RM : 4, GN = RN < 4 ? RN : 4;  // contiguous run of each
+    __shared__ GroupTables tab;
+    __shared__ __align__(16) float sA[2][TK][TM + 4];
+    __shared__ __align__(16) float sB[2][TK][TN + 4];
+    griddep_wait();
+    griddep_launch_dependents();
+    if (threadIdx.x < 32)
+        build_group_tables<FORM == FORM_GW>(p.offsets, p.rows, p.E, TM, p.m_tiles, p.st, &tab, threadIdx.x);
+    __syncthreads();
+    const int tile = blockIdx.x;
+    if (tile >= tab.start[p.E] * p.n_tiles) return;
+    int i = 0;
+    while (tab.start[i + 1] * p.n_tiles <= tile) ++i;
+    const int local = tile - tab.start[i] * p.n_tiles;
+    const int m0 = local / p.n_tiles * TM, n0 = local % p.n_tiles * TN;
+    const int e = tab.expert[i];
+    const int out_n = FORM == FORM_GX ? p.K : p.N;                                   // output columns
+    const int m_n = (FORM == FORM_GW ? p.K : tab.nrows[i]) - m0, n_n = out_n - n0;   // outputs from here
+    const int k_n = FORM == FORM_FWD ? p.K : FORM == FORM_GX ? p.N : tab.nrows[i];   // contraction length
+    const int64_t row0 = tab.row0[i];
+    const float *a, *b;
+    int64_t lda, ldb;
+    if (FORM == FORM_FWD) {
+        a = p.A + (row0 + m0) * p.K;
+        lda = p.K;
+        b = p.B + (int64_t)e * p.K * p.N + n0;
+        ldb = p.N;
+    } else if (FORM == FORM_GX) {
+        a = p.A + (row0 + m0) * p.N;
+        lda = p.N;
+        b = p.B + (int64_t)e * p.K * p.N + (int64_t)n0 * p.N;
+        ldb = p.N;
+    } else {
+        a = p.A + row0 * p.K + m0;
+        lda = p.K;
+        b = p.B + row0 * p.N + n0;
+        ldb = p.N;
+    }
+    Piece<TM, FORM != FORM_GW> pa;
+    Piece<TN, FORM == FORM_GX> pb;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    uint64_t acc[RM][RN / 2];
+#pragma unroll
+    for (int r = 0; r < RM; ++r)
+#pragma unroll
+        for (int c = 0; c < RN / 2; ++c) acc[r][c] = 0ull;
+    pa.load(a, lda, m_n, 0, k_n);
+    pb.load(b, ldb, n_n, 0, k_n);
+    int buf = 0;
+    for (int k0 = 0; k0 < k_n; k0 += TK) {
+        pa.store(sA[buf]);
+        pb.store(sB[buf]);
+        __syncthreads();
+        if (k0 + TK < k_n) {
+            pa.load(a, lda, m_n, k0 + TK, k_n);
+            pb.load(b, ldb, n_n, k0 + TK, k_n);
+        }
+#pragma unroll
+        for (int k = 0; k < TK; ++k) {
+            float av[RM];
+            uint64_t bv[RN / 2];
+#pragma unroll
+            for (int g = 0; g < RM / GM; ++g)
+#pragma unroll
+                for (int j = 0; j < GM; ++j) av[g * GM + j] = sA[buf][k][g * 16 * GM + ty * GM + j];
+#pragma unroll
+            for (int g = 0; g < RN / GN; ++g)
+#pragma unroll
+                for (int j = 0; j < GN / 2; ++j)
+                    bv[g * GN / 2 + j] =
+                        *reinterpret_cast<const uint64_t*>(&sB[buf][k][g * 16 * GN + tx * GN + 2 * j]);
+#pragma unroll
+            for (int r = 0; r < RM; ++r) {
+                const uint64_t ar = pack2(av[r], av[r]);
+#pragma unroll
+                for (int c = 0; c < RN / 2; ++c) acc[r][c] = fma2(ar, bv[c], acc[r][c]);
+            }
+        }
+        buf ^= 1;  // the other buffer was last read before this iteration's barrier
+    }
+#pragma unroll
+    for (int r = 0; r < RM; ++r) {
+        const int m = r / GM * 16 * GM + ty * GM + r % GM;
+        if (m >= m_n) continue;
+        float* orow = p.out + (FORM == FORM_GW ? (int64_t)e * p.K + m0 + m : row0 + m0 + m) * out_n;
+#pragma unroll
+        for (int c = 0; c < RN; c += 2) {
+            const int n = c / GN * 16 * GN + tx * GN + c % GN;
+            if (n >= n_n) continue;  // sizes are multiples of 4: pairs are whole
+            float v0, v1;
+            unpack2(acc[r][c / 2], v0, v1);
+            if (FORM == FORM_FWD && p.bias != nullptr) {
+                v0 += p.bias[(int64_t)e * p.N + n0 + n];
+                v1 += p.bias[(int64_t)e * p.N + n0 + n + 1];
+            }
+            float2* dst = reinterpret_cast<float2*>(orow + n0 + n);
+            if (FORM != FORM_FWD && p.accumulate) {
+                const float2 old = *dst;
+                v0 += old.x;
+                v1 += old.y;
+            }
+            *dst = make_float2(v0, v1);
+        }
+    }
+}
+
+// Outputs of a tile at most; the choice between 128 x 128 and 64 x 64 tiles: the large ones where
+// they fill the device.
+template <int FORM, int TM, int TN>
+cudaError_t launch_tiles(F32Params p, int out_m, int out_n, cudaStream_t s) {
+    p.n_tiles = (out_n + TN - 1) / TN;
+    p.m_tiles = (out_m + TM - 1) / TM;
+    const int64_t row_tiles = FORM == FORM_GW ? (int64_t)p.E * p.m_tiles : (int64_t)p.rows / TM + p.E;
+    return launch_kernel(grouped_f32_kernel<FORM, TM, TN>, dim3((unsigned)(row_tiles * p.n_tiles)), dim3(kF32Threads),
+                         0, s, p);
+}
+
+template <int FORM>
+cudaError_t launch_form(const GroupedArgs& a, const F32Params& p, int out_m, int out_n, cudaStream_t s) {
+    const int64_t big = (FORM == FORM_GW ? (int64_t)a.E * ((out_m + 127) / 128) : (a.rows + 127) / 128) *
+                        ((out_n + 127) / 128);
+    return big >= sm_count() ? launch_tiles<FORM, 128, 128>(p, out_m, out_n, s)
+                             : launch_tiles<FORM, 64, 64>(p, out_m, out_n, s);
+}
+
+F32Params params(const GroupedArgs& a) {
+    F32Params p;
+    p.offsets = a.offsets;
+    p.rows = (int)a.rows;
+    p.E = a.E;
+    p.K = a.K;
+    p.N = a.N;
+    p.accumulate = a.accumulate ? 1 : 0;
+    p.st = a.st;
+    return p;
+}
+
+// ------------------------------------------------------------ bias gradients
+constexpr int kColThreads = 256;  // 8 warps; a lane holds 4 columns
+
+struct ColsumParams {
+    const void* dy = nullptr;
+    void* db = nullptr;
+    const int32_t* offsets = nullptr;
+    int rows = 0, N = 0, accumulate = 0;
+    DevStatus st;
+};
+
+template <bool IN_BF16>
+__device__ __forceinline__ float4 load4(const void* base, int64_t i) {
+    if (IN_BF16) {
+        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(base) + i);
+        return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+    }
+    return *reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
+}
+
+// One CTA per (expert, 128 columns): warp w adds the rows w, w+8, ... of its
+// expert in two interleaved sums, and the sixteen sums of a column are added
+// in a fixed order.
+template <bool IN_BF16, bool OUT_BF16>
+__global__ void __launch_bounds__(kColThreads) colsum_kernel(ColsumParams p) {
+    __shared__ float4 part[8][32];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int e = blockIdx.y, col = blockIdx.x * 128 + lane * 4;
+    int row0, n;
+    group_rows(p.offsets, p.rows, e, p.st, row0, n);
+    float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
+    if (col < p.N) {
+        int r = warp;
+        for (; r + 8 < n; r += 16) {
+            const float4 a = load4<IN_BF16>(p.dy, (int64_t)(row0 + r) * p.N + col);
+            const float4 b = load4<IN_BF16>(p.dy, (int64_t)(row0 + r + 8) * p.N + col);
+            s0.x += a.x, s0.y += a.y, s0.z += a.z, s0.w += a.w;
+            s1.x += b.x, s1.y += b.y, s1.z += b.z, s1.w += b.w;
+        }
+        if (r < n) {
+            const float4 a = load4<IN_BF16>(p.dy, (int64_t)(row0 + r) * p.N + col);
+            s0.x += a.x, s0.y += a.y, s0.z += a.z, s0.w += a.w;
+        }
+    }
+    part[warp][lane] = make_float4(s0.x + s1.x, s0.y + s1.y, s0.z + s1.z, s0.w + s1.w);
+    __syncthreads();
+    if (threadIdx.x < 128) {
+        const int c = blockIdx.x * 128 + threadIdx.x;
+        if (c >= p.N) return;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) v += reinterpret_cast<const float*>(part[w])[threadIdx.x];
+        const int64_t o = (int64_t)e * p.N + c;
+        if (OUT_BF16) {
+            __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.db) + o;
+            if (p.accumulate) v += __bfloat162float(*d);
+            *d = __float2bfloat16_rn(v);
+        } else {
+            float* d = static_cast<float*>(p.db) + o;
+            if (p.accumulate) v += *d;
+            *d = v;
+        }
+    }
+}
+
+// ------------------------------------------------------- fp32 activation gradient
+template <bool SWIGLU>
+__global__ void __launch_bounds__(256) act_grad_f32_kernel(int64_t n, float* g, float* u, float* dh) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    const float x = g[i], d = dh[i];
+    if (SWIGLU) {
+        const float s = 1.0f / (1.0f + expf(-x)), xs = x * s, uv = u[i];
+        dh[i] = xs * uv;
+        g[i] = d * uv * (s + xs * (1.0f - s));
+        u[i] = d * xs;
+    } else {
+        const float cdf = 0.5f * (1.0f + erff(x * 0.70710678118654752f));
+        dh[i] = x * cdf;
+        g[i] = d * (cdf + x * 0.39894228040143268f * expf(-0.5f * x * x));
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_grouped_fwd_f32(const GroupedArgs& a, cudaStream_t s) {
+    F32Params p = params(a);
+    p.accumulate = 0;
+    p.A = static_cast<const float*>(a.x);
+    p.B = static_cast<const float*>(a.w);
+    p.bias = static_cast<const float*>(a.bias);
+    p.out = static_cast<float*>(a.y);
+    return launch_form<FORM_FWD>(a, p, 0, a.N, s);
+}
+
+cudaError_t launch_grouped_gx_f32(const GroupedArgs& a, cudaStream_t s) {
+    F32Params p = params(a);
+    p.A = static_cast<const float*>(a.dy);
+    p.B = static_cast<const float*>(a.w);
+    p.out = static_cast<float*>(a.dx);
+    return launch_form<FORM_GX>(a, p, 0, a.K, s);
+}
+
+cudaError_t launch_grouped_gw_f32(const GroupedArgs& a, cudaStream_t s) {
+    F32Params p = params(a);
+    p.A = static_cast<const float*>(a.x);
+    p.B = static_cast<const float*>(a.dy);
+    p.out = static_cast<float*>(a.dw);
+    return launch_form<FORM_GW>(a, p, a.K, a.N, s);
+}
+
+cudaError_t launch_grouped_colsum(const GroupedArgs& a, bool dy_bf16, cudaStream_t s) {
+    ColsumParams p;
+    p.dy = a.dy;
+    p.db = a.db;
+    p.offsets = a.offsets;
+    p.rows = (int)a.rows;
+    p.N = a.N;
+    p.accumulate = a.accumulate ? 1 : 0;
+    p.st = a.st;
+    const dim3 grid((unsigned)((a.N + 127) / 128), (unsigned)a.E), block(kColThreads);
+    if (!dy_bf16) return launch_kernel(colsum_kernel<false, false>, grid, block, 0, s, p);
+    return a.out_f32 ? launch_kernel(colsum_kernel<true, false>, grid, block, 0, s, p)
+                     : launch_kernel(colsum_kernel<true, true>, grid, block, 0, s, p);
+}
+
+cudaError_t launch_act_grad_f32(int act, int64_t n, float* g, float* u, float* dh, cudaStream_t s) {
+    if (n <= 0) return cudaSuccess;
+    const dim3 grid((unsigned)((n + 255) / 256));
+    return act == 0 ? launch_kernel(act_grad_f32_kernel<true>, grid, dim3(256), 0, s, n, g, u, dh)
+                    : launch_kernel(act_grad_f32_kernel<false>, grid, dim3(256), 0, s, n, g, u, dh);
+}
+
+}  // namespace moe

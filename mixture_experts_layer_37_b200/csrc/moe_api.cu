@@ -6,6 +6,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include "grouped.h"
 #include "internal.h"
 #include "moe.h"
 
@@ -1018,6 +1019,272 @@ int32_t moe_forward_launch_count(const moe_config_t* cfg) {
     if (check_config(cfg) != MOE_OK) return 0;
     if (cfg->T == 0) return 1;
     return 5 + 2 * cfg->n_shared;  // router, scatter, two GEMMs, combine; two GEMMs per shared expert
+}
+
+}  // extern "C"
+
+// ---- grouped products and the expert FFN's backward pass
+namespace {
+
+moe_status_t check_grouped(const moe_grouped_config_t* g) {
+    if (g == nullptr) return MOE_ERR_INVALID_ARG;
+    if (g->rows < 0 || g->E <= 0 || g->K <= 0 || g->N <= 0) return MOE_ERR_INVALID_ARG;
+    if (g->dtype != MOE_DT_F32 && g->dtype != MOE_DT_BF16) return MOE_ERR_INVALID_ARG;
+    if (g->E > kMaxExperts || g->rows >= ((int64_t)1 << 31) - 1024) return MOE_ERR_UNSUPPORTED;
+    const int step = g->dtype == MOE_DT_BF16 ? 8 : 4;  // rows of 16-byte pieces
+    if (g->K % step != 0 || g->N % step != 0) return MOE_ERR_UNSUPPORTED;
+    // strides of the tensor maps stay below 2^40 bytes, tile numbers below 2^31 (64 x 64 tiles at least)
+    const int64_t lim = (int64_t)1 << 31;
+    const int64_t kt = (g->K + 63) / 64, nt = (g->N + 63) / 64, mt = g->rows / 64 + g->E;
+    if ((int64_t)g->K * g->N >= ((int64_t)1 << 38)) return MOE_ERR_UNSUPPORTED;
+    if (kt * nt * g->E >= lim || mt * kt >= lim || mt * nt >= lim) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+moe_status_t check_grouped_ws(const void* ws, size_t ws_bytes, size_t need) {
+    if (ws == nullptr || ws_bytes < need) return MOE_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(ws) & 1023u) != 0) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+bool given(const void* p) { return p != nullptr && aligned16(p); }
+
+GroupedArgs grouped_args(const moe_grouped_config_t* g, const int32_t* offsets, void* ws) {
+    GroupedArgs a;
+    a.offsets = offsets;
+    a.rows = g->rows;
+    a.E = g->E;
+    a.K = g->K;
+    a.N = g->N;
+    a.st = status_of(ws);
+    return a;
+}
+
+cudaError_t grouped_fwd(const GroupedArgs& a, bool bf16, cudaStream_t s) {
+    return bf16 ? launch_grouped_fwd_bf16(a, s) : launch_grouped_fwd_f32(a, s);
+}
+cudaError_t grouped_gx(const GroupedArgs& a, bool bf16, cudaStream_t s) {
+    return bf16 ? launch_grouped_gx_bf16(a, s) : launch_grouped_gx_f32(a, s);
+}
+// dW and db; db after dw on the stream.
+cudaError_t grouped_gw(const GroupedArgs& a, bool bf16, cudaStream_t s) {
+    if (a.dw != nullptr) {
+        const cudaError_t err = bf16 ? launch_grouped_gw_bf16(a, s) : launch_grouped_gw_f32(a, s);
+        if (err != cudaSuccess) return err;
+    }
+    if (a.db == nullptr) return cudaSuccess;
+    return launch_grouped_colsum(a, bf16, s);
+}
+
+struct BackwardPlan {
+    size_t dh, h, d0, d1, total;
+};
+BackwardPlan backward_plan(const moe_config_t* c) {
+    const size_t n = (size_t)max_rows(c) * c->ffn, s = elem_size(c);
+    BackwardPlan p;
+    size_t off = kStatusBytes;
+    p.dh = off;  // fp32: the gradient of the inner activation (f32: then the activation itself)
+    off = align_up(off + n * 4, 1024);
+    p.h = off;   // bf16: the inner activation
+    off = align_up(off + (c->dtype == MOE_DT_BF16 ? n * s : 0), 1024);
+    p.d0 = off;  // gradient of gate, or of the GELU's argument (f32: first that value itself)
+    off = align_up(off + n * s, 1024);
+    p.d1 = off;  // gradient of up
+    off = align_up(off + (c->act == MOE_ACT_SWIGLU ? n * s : 0), 1024);
+    p.total = off;
+    return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_grouped_workspace_size(const moe_grouped_config_t* cfg, size_t* bytes) {
+    const moe_status_t st = check_grouped(cfg);
+    if (st != MOE_OK) return st;
+    if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+    *bytes = kStatusBytes;
+    return MOE_OK;
+}
+
+moe_status_t moe_grouped_gemm(const moe_grouped_config_t* cfg, const void* x, const void* w, const void* bias,
+                              const int32_t* offsets, void* y, void* ws, size_t ws_bytes, cudaStream_t stream) {
+    moe_status_t st = check_grouped(cfg);
+    if (st != MOE_OK) return st;
+    if (!given(w) || offsets == nullptr || !aligned16(bias)) return MOE_ERR_INVALID_ARG;
+    if (cfg->rows > 0 && (!given(x) || !given(y))) return MOE_ERR_INVALID_ARG;
+    if ((st = check_grouped_ws(ws, ws_bytes, kStatusBytes)) != MOE_OK) return st;
+    if (cfg->rows == 0) return MOE_OK;
+    GroupedArgs a = grouped_args(cfg, offsets, ws);
+    a.x = x;
+    a.w = w;
+    a.bias = bias;
+    a.y = y;
+    return from_cuda(grouped_fwd(a, cfg->dtype == MOE_DT_BF16, stream));
+}
+
+moe_status_t moe_grouped_gemm_grad_x(const moe_grouped_config_t* cfg, const void* dy, const void* w,
+                                     const int32_t* offsets, void* dx, void* ws, size_t ws_bytes,
+                                     cudaStream_t stream) {
+    moe_status_t st = check_grouped(cfg);
+    if (st != MOE_OK) return st;
+    if (!given(w) || offsets == nullptr) return MOE_ERR_INVALID_ARG;
+    if (cfg->rows > 0 && (!given(dy) || !given(dx))) return MOE_ERR_INVALID_ARG;
+    if ((st = check_grouped_ws(ws, ws_bytes, kStatusBytes)) != MOE_OK) return st;
+    if (cfg->rows == 0) return MOE_OK;
+    GroupedArgs a = grouped_args(cfg, offsets, ws);
+    a.dy = dy;
+    a.w = w;
+    a.dx = dx;
+    return from_cuda(grouped_gx(a, cfg->dtype == MOE_DT_BF16, stream));
+}
+
+moe_status_t moe_grouped_gemm_grad_w(const moe_grouped_config_t* cfg, const void* x, const void* dy,
+                                     const int32_t* offsets, void* dw, void* db, int32_t grad_dtype,
+                                     int32_t accumulate, void* ws, size_t ws_bytes, cudaStream_t stream) {
+    moe_status_t st = check_grouped(cfg);
+    if (st != MOE_OK) return st;
+    if (grad_dtype != MOE_DT_F32 && grad_dtype != cfg->dtype) return MOE_ERR_INVALID_ARG;
+    if (!given(dw) || offsets == nullptr || !aligned16(db)) return MOE_ERR_INVALID_ARG;
+    if (cfg->rows > 0 && (!given(x) || !given(dy))) return MOE_ERR_INVALID_ARG;
+    if ((st = check_grouped_ws(ws, ws_bytes, kStatusBytes)) != MOE_OK) return st;
+    if (cfg->rows == 0) {
+        if (accumulate != 0) return MOE_OK;
+        const size_t es = grad_dtype == MOE_DT_F32 ? 4 : 2, n = (size_t)cfg->E * cfg->N;
+        cudaError_t err = cudaMemsetAsync(dw, 0, n * cfg->K * es, stream);
+        if (err == cudaSuccess && db != nullptr) err = cudaMemsetAsync(db, 0, n * es, stream);
+        return from_cuda(err);
+    }
+    GroupedArgs a = grouped_args(cfg, offsets, ws);
+    a.x = x;
+    a.dy = dy;
+    a.dw = dw;
+    a.db = db;
+    a.out_f32 = grad_dtype == MOE_DT_F32;
+    a.accumulate = accumulate != 0;
+    return from_cuda(grouped_gw(a, cfg->dtype == MOE_DT_BF16, stream));
+}
+
+moe_status_t moe_expert_ffn_backward_workspace_size(const moe_config_t* cfg, size_t* bytes) {
+    const moe_status_t st = check_config(cfg);
+    if (st != MOE_OK) return st;
+    if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+    *bytes = backward_plan(cfg).total;
+    return MOE_OK;
+}
+
+moe_status_t moe_expert_ffn_backward(const moe_config_t* cfg, const moe_weights_t* weights, const void* x_perm,
+                                     const int32_t* offsets, const void* dy_perm, const moe_ffn_grads_t* grads,
+                                     void* ws, size_t ws_bytes, cudaStream_t stream) {
+    moe_status_t st = check_config(cfg);
+    if (st != MOE_OK) return st;
+    if (cfg->weight_format != MOE_WEIGHTS_NATIVE) return MOE_ERR_UNSUPPORTED;
+    moe_config_t c = *cfg;
+    c.n_shared = 0;  // the routed experts alone
+    if ((st = check_weights(&c, weights, false, true)) != MOE_OK) return st;
+    const bool swiglu = cfg->act == MOE_ACT_SWIGLU, bf16 = cfg->dtype == MOE_DT_BF16;
+    if (grads == nullptr || offsets == nullptr) return MOE_ERR_INVALID_ARG;
+    if (grads->grad_dtype != MOE_DT_F32 && grads->grad_dtype != cfg->dtype) return MOE_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)grads->dx, (const void*)grads->w_gate_or_w1, (const void*)grads->w_up,
+                          (const void*)grads->w_down_or_w2, (const void*)grads->b1, (const void*)grads->b2})
+        if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+    const int64_t rows = max_rows(cfg);
+    if (rows > 0 && (!given(x_perm) || !given(dy_perm))) return MOE_ERR_INVALID_ARG;
+    moe_grouped_config_t g1 = {rows, cfg->E, cfg->d, cfg->ffn, cfg->dtype};  // [E, d, ffn]
+    moe_grouped_config_t g2 = {rows, cfg->E, cfg->ffn, cfg->d, cfg->dtype};  // [E, ffn, d]
+    if ((st = check_grouped(&g1)) != MOE_OK) return st;
+    const BackwardPlan pl = backward_plan(cfg);
+    if ((st = check_grouped_ws(ws, ws_bytes, pl.total)) != MOE_OK) return st;
+    void* db1 = swiglu ? nullptr : grads->b1;
+    void* db2 = swiglu ? nullptr : grads->b2;
+    void* dw_up = swiglu ? grads->w_up : nullptr;
+    if (rows == 0) {
+        if (grads->accumulate != 0) return MOE_OK;
+        const size_t es = grads->grad_dtype == MOE_DT_F32 ? 4 : 2, E = (size_t)cfg->E;
+        const size_t n = E * cfg->d * cfg->ffn * es;
+        const std::pair<void*, size_t> clear[] = {{grads->w_gate_or_w1, n}, {dw_up, n}, {grads->w_down_or_w2, n},
+                                                  {db1, E * cfg->ffn * es}, {db2, E * cfg->d * es}};
+        for (const auto& z : clear)
+            if (z.first != nullptr && cudaMemsetAsync(z.first, 0, z.second, stream) != cudaSuccess) return MOE_ERR_CUDA;
+        return MOE_OK;
+    }
+    const NvtxRange range("moe_expert_ffn_backward");
+    GroupedArgs in = grouped_args(&g1, offsets, ws), out = grouped_args(&g2, offsets, ws);
+    in.out_f32 = out.out_f32 = grads->grad_dtype == MOE_DT_F32;
+    in.accumulate = out.accumulate = grads->accumulate != 0;
+    void* const dh = at(ws, pl.dh);
+    void* const h = bf16 ? (void*)at(ws, pl.h) : dh;
+    void* const d0 = at(ws, pl.d0);
+    void* const d1 = swiglu ? (void*)at(ws, pl.d1) : nullptr;
+    // the gradient of the inner activation: dh = dy W2^T, fp32
+    GroupedArgs a = out;
+    a.dy = dy_perm;
+    a.w = weights->w_down_or_w2;
+    a.dx = dh;
+    a.out_f32 = true;
+    a.accumulate = false;
+    if (grouped_gx(a, bf16, stream) != cudaSuccess) return MOE_ERR_CUDA;
+    const PdlScope pdl;  // the launches after the first overlap each predecessor's tail
+    // the inner products again, and the activation's gradient
+    a = in;
+    a.x = x_perm;
+    a.w = weights->w_gate_or_w1;
+    a.bias = swiglu ? nullptr : weights->b1;
+    if (bf16) {
+        a.w2 = weights->w_up;
+        a.grad_act = swiglu ? GRAD_SWIGLU : GRAD_GELU;
+        a.dh = dh;
+        a.h = h;
+        a.d0 = d0;
+        a.d1 = d1;
+        if (launch_grouped_fwd_bf16(a, stream) != cudaSuccess) return MOE_ERR_CUDA;
+    } else {
+        a.y = d0;
+        if (launch_grouped_fwd_f32(a, stream) != cudaSuccess) return MOE_ERR_CUDA;
+        if (swiglu) {
+            a.w = weights->w_up;
+            a.y = d1;
+            if (launch_grouped_fwd_f32(a, stream) != cudaSuccess) return MOE_ERR_CUDA;
+        }
+        if (launch_act_grad_f32(cfg->act, rows * cfg->ffn, static_cast<float*>(d0), static_cast<float*>(d1),
+                                static_cast<float*>(dh), stream) != cudaSuccess)
+            return MOE_ERR_CUDA;
+    }
+    // gradients of the matrices and biases
+    out.x = h;
+    out.dy = dy_perm;
+    out.dw = grads->w_down_or_w2;
+    out.db = db2;
+    if (grouped_gw(out, bf16, stream) != cudaSuccess) return MOE_ERR_CUDA;
+    in.x = x_perm;
+    in.dy = d0;
+    in.dw = grads->w_gate_or_w1;
+    in.db = db1;
+    if (grouped_gw(in, bf16, stream) != cudaSuccess) return MOE_ERR_CUDA;
+    in.dy = d1;
+    in.dw = dw_up;
+    in.db = nullptr;
+    if (grouped_gw(in, bf16, stream) != cudaSuccess) return MOE_ERR_CUDA;
+    if (grads->dx == nullptr) return MOE_OK;
+    // the gradient of the rows; SwiGLU: both pairs in one sum
+    a = in;
+    a.out_f32 = !bf16;
+    a.accumulate = false;
+    a.dy = d0;
+    a.w = weights->w_gate_or_w1;
+    a.dx = grads->dx;
+    if (bf16 && swiglu) {
+        a.dy2 = d1;
+        a.w2 = weights->w_up;
+    }
+    if (grouped_gx(a, bf16, stream) != cudaSuccess) return MOE_ERR_CUDA;
+    if (!bf16 && swiglu) {
+        a.dy = d1;
+        a.w = weights->w_up;
+        a.accumulate = true;
+        if (grouped_gx(a, bf16, stream) != cudaSuccess) return MOE_ERR_CUDA;
+    }
+    return MOE_OK;
 }
 
 }  // extern "C"
