@@ -10,29 +10,49 @@
 // balancing, capacity factor" (dpshk.com/news/6005940) §2.2, §4.4; gradients
 // from the product rule).
 //
-// One persistent CTA per SM, 192 threads: warp 0 loads by TMA, warp 1 issues
-// tcgen05.mma (M=128, N=256, K=16, two TMEM accumulators of 256 columns), warps
-// 2-5 read the accumulators and store.  What differs between the three forms
-// is which operand is contiguous along the contraction:
-//   FWD  A = x rows, contraction-major; B = W[e], output-major (four boxes
-//        [64 k x 64 n]);
+// Persistent CTA pairs (tcgen05 cta_group::2): a cluster of two CTAs computes
+// one 256 x 256 tile, each holding 128 of its rows and 128 of its columns in
+// shared memory; 352 threads per CTA: warp 0 loads by TMA, one lane of warp 1
+// of the leader issues the MMAs (M=256, N=256, K=16, two TMEM accumulators of
+// 256 columns), warps 2-9 read the CTA's 128 accumulator rows and store, warp
+// 10 clears rows (GW, below).
+// Why pairs: one CTA with a 128 x 256 tile reads 12 KB of operands from shared
+// memory for each MMA of 128 clocks and receives as much by TMA, 24 KB where
+// the memory moves 16; measured, its tensor pipe stood at 72 % for any pipeline
+// depth.  A pair moves 8 KB + 8 KB per SM for the same work.
+// What differs between the three forms is which operand is contiguous along
+// the contraction:
+//   FWD  A = x rows, contraction-major; B = W[e], output-major (two boxes
+//        [64 k x 64 n] per CTA);
 //   GX   A = dy rows, contraction-major; B = W[e], contraction-major (one box
-//        [256 k x 64 n]): the weights are read as they lie, nothing is transposed;
-//   GW   both output-major: A = x (two boxes [64 rows x 64 k]), B = dy (four
-//        boxes [64 rows x 64 n]); the contraction runs over the expert's rows.
+//        [128 k x 64 n] per CTA): the weights are read as they lie;
+//   GW   both output-major: A = x (two boxes [64 rows x 64 k] per CTA), B = dy
+//        (two boxes [64 rows x 64 n]); the contraction runs over the expert's rows.
 // Weights and weight gradients are addressed as 3-D tensors [E, K, N], so a K
-// or N that fills no tile is cut at the expert's own edge (zero fill on loads)
-// and never mixes with the next expert's values.
+// or N that fills no tile is cut at the expert's own edge (zero fill on loads,
+// clipping on stores) and never mixes with the next expert's values.
 //
 // Ragged edges.  FWD, GX: a tile that runs past its expert's last row reads
 // the next rows and does not store them (rows do not mix).  GW: rows of the
 // next expert in the last block of 64 would be summed, and 0 * inf is not 0, so
-// they are not multiplied by zero but overwritten: the MMA warp clears the rows
-// of both operands behind the expert's end up to the next multiple of 16 in
-// shared memory (at most 15 rows, once per tile) and issues only that many
-// K=16 steps.  GW tiles are taken expert by expert in order of falling row
-// count, so that the last wave holds the cheapest tiles.
+// they are not multiplied by zero but overwritten: warp 10 of each CTA clears
+// the rows of its operands behind the expert's end up to the next multiple of
+// 16 in shared memory (at most 15 rows, once per tile) and only that many K=16
+// steps are issued.  The last block of an expert therefore lands on a barrier
+// of each CTA's own, and the leader waits for the clearing warps of both CTAs
+// instead of the copies.  GW tiles are taken expert by expert in order
+// of falling row count, so that the last wave holds the cheapest tiles.
+// A last tile of at most 128 rows (GW: output rows) runs as an M=128 pair: 64
+// rows per CTA, its accumulator in TMEM lanes 0-63 for the first 128 columns
+// and 64-127 for the others.
+//
+// Stores go through shared memory: a warp's 32 rows of 128 bytes, then one TMA
+// store (or fp32 reduction, when accumulating), or, for a warp with fewer rows,
+// whole lines by eight lanes per row.  (Lanes storing their own rows 16 bytes
+// at a time moved three times the sectors.)
 // Every wait is bounded in time, as in the other kernels.
+#include <type_traits>
+
 #include "gemm_common.cuh"
 #include "grouped.h"
 
@@ -41,18 +61,32 @@ namespace {
 
 using namespace gemm;
 
-constexpr int BM = 128;
-constexpr int kStages = 4;
-constexpr int kAStageBytes = BM * BK * 2;                 // 16 KB
-constexpr int kBStageBytes = 4 * kBBoxBytes;              // 32 KB
-constexpr int kStageBytes = kAStageBytes + kBStageBytes;  // 48 KB
-constexpr int kSmemBytes = kStages * kStageBytes + 1024 /*barriers, tables*/ + 1024 /*alignment*/;
+constexpr int BM = 256;                                   // tile rows (128 per CTA)
+constexpr int kGroupM2 = 16;                              // m-tiles per raster group
+constexpr int kABytes = 128 * BK * 2;                     // 16 KB: this CTA's rows of A
+constexpr int kBBytes = 2 * kBBoxBytes;                   // 16 KB: this CTA's columns of B
+constexpr int kStageBytes = kABytes + kBBytes;            // 32 KB
+constexpr int kEpiWarps = 8;                              // two per 32 TMEM lanes: one for each half of the columns
+constexpr int kClearWarp = 2 + kEpiWarps;                // GW: clears the rows behind an expert's end
+constexpr int kThreadsG = 32 * (kClearWarp + 1);
+constexpr int kSlabBytes = 32 * 128;                      // an epilogue warp's staging: 32 rows of 128 bytes
+constexpr int kRunRows = 512;                             // GW, fp32 output: rows summed in TMEM before a promotion
 
 enum { FORM_FWD = 0, FORM_GX = 1, FORM_GW = 2 };
 // What the epilogue does with the fp32 accumulators: round to bf16 (with a
 // bias in FWD, added to what is there in GW on request), store as fp32, or, in
 // FWD, the backward pass of the expert activation (below).
 enum { EPI_BF16 = 0, EPI_F32 = 1, EPI_SWIGLU_GRAD = 2, EPI_GELU_GRAD = 3 };
+
+// fp32 outputs take twice the stores of a bf16 tile: two staging slabs per warp, one stage less.
+template <int EPI>
+struct Smem {
+    static constexpr int kSlabs = EPI == EPI_F32 ? 2 : 1;
+    static constexpr int kStages = EPI == EPI_F32 ? 5 : 6;
+    static constexpr int kSlabOff = kStages * kStageBytes;
+    static constexpr int kBarOff = kSlabOff + kEpiWarps * kSlabs * kSlabBytes;
+    static constexpr int kBytes = kBarOff + 256 + 1024 /*alignment*/;
+};
 
 struct GroupedParams {
     const int32_t* offsets = nullptr;  // [E+1]
@@ -77,41 +111,45 @@ constexpr uint32_t make_idesc_majors(int m, int n, bool a_mn, bool b_mn) {
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-__device__ __forceinline__ void tma_load_3d(void* smem_dst, const void* map, uint64_t* bar, int32_t c0, int32_t c1,
-                                            int32_t c2) {
+// tma_load_2d_pair with three coordinates.
+__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const void* map, uint32_t bar_cluster_addr, int32_t c0,
+                                                 int32_t c1, int32_t c2) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
-            smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+        "%5}], [%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster_addr), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
 }
 
 struct Tile {
     int e, m0, row0, rows, nt;  // FWD, GX: rows of this tile from row0; GW: m0 in the output, rows to sum from row0
+    bool half;                  // an M=128 pair
 };
 
-// Expert by expert; inside an expert groups of kGroupM m-tiles, n-tile-major
-// inside a group, so that the CTAs running together share operands in L2.
+// Expert by expert; inside an expert groups of kGroupM2 m-tiles, n-tile-major
+// inside a group, so that the pairs running together share operands in L2.
+// `i`: the caller's place in the tables; its tiles only grow.
 template <int FORM>
-__device__ __forceinline__ Tile decode(int tile, const GroupedParams& p, const GroupTables* t) {
-    int i = 0;
+__device__ __forceinline__ Tile decode(int tile, const GroupedParams& p, const GroupTables* t, int& i) {
     while (t->start[i + 1] * p.n_tiles <= tile) ++i;
     const int local = tile - t->start[i] * p.n_tiles;
     const int mt_e = t->start[i + 1] - t->start[i];
-    const int grp = local / (kGroupM * p.n_tiles);
-    const int gm = min(kGroupM, mt_e - grp * kGroupM);
-    const int r = local - grp * kGroupM * p.n_tiles;
+    const int grp = local / (kGroupM2 * p.n_tiles);
+    const int gm = min(kGroupM2, mt_e - grp * kGroupM2);
+    const int r = local - grp * kGroupM2 * p.n_tiles;
     Tile o;
     o.nt = r / gm;
-    const int mt = grp * kGroupM + (r - o.nt * gm);
+    const int mt = grp * kGroupM2 + (r - o.nt * gm);
     o.e = t->expert[i];
     o.m0 = mt * BM;
     if (FORM == FORM_GW) {
         o.row0 = t->row0[i];
         o.rows = t->nrows[i];
+        o.half = p.M - o.m0 <= BM / 2;
     } else {
         o.row0 = t->row0[i] + o.m0;
         o.rows = min(BM, t->nrows[i] - o.m0);
+        o.half = o.rows <= BM / 2;
     }
     return o;
 }
@@ -121,15 +159,98 @@ __device__ __forceinline__ int tile_kblocks(const GroupedParams& p, const Tile& 
     return FORM == FORM_GW ? (t.rows + BK - 1) / BK : p.kblocks + p.kblocks2;
 }
 
-__device__ __forceinline__ void store16_bf16(__nv_bfloat16* row, int col, int N, const float* x) {
+// A slab: 32 rows (one per lane) of 128 bytes in shared memory, 16-byte pieces
+// permuted by the row so that both a lane writing its row and eight lanes
+// reading one row touch all banks once.
+__device__ __forceinline__ uint4* slab_piece(uint8_t* slab, int row, int piece) {
+    return reinterpret_cast<uint4*>(slab + row * 128 + ((piece ^ (row & 7)) << 4));
+}
+__device__ __forceinline__ uint4 pack8_bf16(const float* v) {
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ uint4 pack4_f32(const float* v) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+// The slab to memory by eight lanes per row.  row(r) says where row r's first
+// column lies, or null where the row is not stored; n = columns left from there.
+template <class T, class Row>
+__device__ __forceinline__ void store_slab(uint8_t* slab, int lane, int n, Row&& row) {
+    __syncwarp();
+    const int piece = lane & 7;
+    constexpr int kPer = 16 / sizeof(T);
 #pragma unroll
-    for (int hlf = 0; hlf < 2; ++hlf)
-        if (col + 8 * hlf < N) {
-            const float* v = x + 8 * hlf;
-            *reinterpret_cast<uint4*>(row + col + 8 * hlf) =
-                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                           pack_bf16x2(v[6], v[7]));
-        }
+    for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + (lane >> 3);
+        const uint4 v = *slab_piece(slab, r, piece);
+        T* dst = row(r);
+        if (dst != nullptr && piece * kPer < n) *reinterpret_cast<uint4*>(dst + piece * kPer) = v;
+    }
+    __syncwarp();
+}
+// The reverse: 32 rows of 128 bytes into registers (zeros where there is no
+// row or column), and from there into the slab.
+template <class T, class Row>
+__device__ __forceinline__ void fetch_rows(uint4 (&v)[8], int lane, int n, Row&& row) {
+    const int piece = lane & 7;
+    constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const T* src = row(4 * i + (lane >> 3));
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (src != nullptr && piece * kPer < n) v[i] = *reinterpret_cast<const uint4*>(src + piece * kPer);
+    }
+}
+__device__ __forceinline__ void put_rows(uint8_t* slab, int lane, const uint4 (&v)[8]) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) *slab_piece(slab, 4 * i + (lane >> 3), lane & 7) = v[i];
+    __syncwarp();
+}
+
+// A slab by TMA: to [.., col..] of row `row` (of expert e where the tensor has
+// three dimensions), or added to it (fp32).  One lane.
+template <bool THREE, bool ADD>
+__device__ __forceinline__ void tma_store(const void* map, const uint8_t* slab, int col, int row, int e) {
+    const uint64_t m = reinterpret_cast<uint64_t>(map);
+    const uint32_t sa = smem_u32(slab);
+    if (THREE && ADD)
+        asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(m),
+                     "r"(sa), "r"(col), "r"(row), "r"(e)
+                     : "memory");
+    else if (THREE)
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(m),
+                     "r"(sa), "r"(col), "r"(row), "r"(e)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(m), "r"(sa),
+                     "r"(col), "r"(row)
+                     : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// At most N of this thread's stores still read their slabs.
+template <int N>
+__device__ __forceinline__ void tma_store_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void tma_store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// mbar_wait_bounded for a phase that the other CTA's threads complete after
+// writing its shared memory: acquires at cluster scope.
+__device__ __forceinline__ bool mbar_wait_bounded_cluster(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
+    const uint64_t t0 = globaltimer_ns();
+    uint32_t n = 0;
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((++n & 15u) == 0 && globaltimer_ns() - t0 > timeout_ns) return false;
+    }
 }
 
 // x += 16 bf16 values at row + col (those inside N).
@@ -167,34 +288,43 @@ __device__ __forceinline__ void gelu_grad(float p, float dh, float& h, float& dp
 }
 
 template <int FORM, int EPI>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmA2, const __grid_constant__ CUtensorMap tmB2,
-                   GroupedParams p) {
-    constexpr bool kTwoB = EPI == EPI_SWIGLU_GRAD;  // gate and up halves of the 256 columns
+                   const __grid_constant__ CUtensorMap tmO, GroupedParams p) {
+    using S = Smem<EPI>;
+    constexpr int kStages = S::kStages;
+    constexpr bool kTwoB = EPI == EPI_SWIGLU_GRAD;  // gate and up halves of each CTA's columns
+    constexpr bool kGw = FORM == FORM_GW;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* sA = smem;
-    uint8_t* sB = smem + kStages * kAStageBytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+    uint8_t* sB = smem + kStages * kABytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBarOff);
     uint64_t* empty = full + kStages;
     uint64_t* tfull = empty + kStages;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* tail = drain + 1;  // [stage] GW: this CTA's part of an expert's last, partly filled block
+    uint64_t* ready = tail + kStages;  // [stage] GW, leader: both CTAs have cleared such a block
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ready + kStages);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     __shared__ GroupTables tab;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank();
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
+            mbar_init(&tail[s], 1);
+            mbar_init(&ready[s], 2);
         }
         mbar_init(&tfull[0], 1);
         mbar_init(&tfull[1], 1);
-        mbar_init(&tempty[0], 4);
-        mbar_init(&tempty[1], 4);
+        mbar_init(&tempty[0], 2 * kEpiWarps);
+        mbar_init(&tempty[1], 2 * kEpiWarps);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -203,19 +333,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tmB);
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, kTmemCols);
-        tmem_relinquish();
+        tmem_alloc_pair(tmem_slot, kTmemCols);
+        tmem_relinquish_pair();
     }
     // the prologue above overlaps the launch before; from here on its results are read
     griddep_wait();
     griddep_launch_dependents();
-    if (warp == 2) build_group_tables<FORM == FORM_GW>(p.offsets, p.rows, p.E, BM, p.m_tiles, p.st, &tab, lane);
+    if (warp == 2) build_group_tables<kGw>(p.offsets, p.rows, p.E, BM, p.m_tiles, p.st, &tab, lane);
     tc_fence_before();
     __syncthreads();
+    cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA signal
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const int total_tiles = tab.start[p.E] * p.n_tiles;
     const uint64_t tmo = p.st.timeout_ns;
+    const uint32_t full_lead = mapa_shared(smem_u32(full), 0);      // the leader's full[0]
+    const uint32_t ready_lead = mapa_shared(smem_u32(ready), 0);    // the leader's ready[0]
+    const uint32_t tempty_lead = mapa_shared(smem_u32(tempty), 0);  // the leader's tempty[0]
 
     auto give_up = [&](uint32_t site) {
         report_timeout(p.st, site);
@@ -224,46 +358,55 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         if (lane == 0) {
-            // ------------------------------------------------ TMA producer
-            int stage = 0;
+            // ------------------------------------------------ TMA producer (both CTAs)
+            int stage = 0, place = 0;
             uint32_t phase = 0, issued_mask = 0, issued_par = 0;
             bool stop = false;
-            for (int tile = blockIdx.x; tile < total_tiles && !stop; tile += gridDim.x) {
-                const Tile t = decode<FORM>(tile, p, &tab);
-                const int n0 = t.nt * p.bn_out;
+            for (int tile = pair; tile < total_tiles && !stop; tile += npairs) {
+                const Tile t = decode<FORM>(tile, p, &tab, place);
                 const int kbs = tile_kblocks<FORM>(p, t);
+                const int own = (t.half ? 64 : 128) * rank;                    // this CTA's rows of the tile
+                const int n0 = t.nt * p.bn_out + (kTwoB ? 64 : 128) * rank;    // and its columns
+                if (*abort_flag) break;
                 for (int kb = 0; kb < kbs; ++kb) {
-                    if (*abort_flag) { stop = true; break; }
                     if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, tmo)) {
                         give_up(SITE_GEMM_PRODUCER_EMPTY);
                         stop = true;
                         break;
                     }
-                    mbar_arrive_expect_tx(&full[stage], kStageBytes);
-                    uint8_t* a_dst = sA + stage * kAStageBytes;
-                    uint8_t* b_dst = sB + stage * kBStageBytes;
-                    if (FORM == FORM_GW) {
+                    uint8_t* a_dst = sA + stage * kABytes;
+                    uint8_t* b_dst = sB + stage * kBBytes;
+                    const uint32_t bar = full_lead + 8u * stage;
+                    if (kGw) {
                         const int r = t.row0 + kb * BK;
+                        if (t.rows - kb * BK < BK) {
+                            // the expert's last, partly filled block: cleared before it counts as full
+                            mbar_arrive_expect_tx(&tail[stage], kStageBytes);
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            tma_load_2d(a_dst + i * kBBoxBytes, &tmA, &full[stage], t.m0 + 64 * i, r);
+                            for (int i = 0; i < 2; ++i) {
+                                tma_load_2d(a_dst + i * kBBoxBytes, &tmA, &tail[stage], t.m0 + own + 64 * i, r);
+                                tma_load_2d(b_dst + i * kBBoxBytes, &tmB, &tail[stage], n0 + 64 * i, r);
+                            }
+                        } else {
+                            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            tma_load_2d(b_dst + i * kBBoxBytes, &tmB, &full[stage], n0 + 64 * i, r);
-                    } else if (FORM == FORM_GX) {
-                        const bool second = kb >= p.kblocks;
-                        const int c = (second ? kb - p.kblocks : kb) * BK;
-                        tma_load_2d(a_dst, second ? &tmA2 : &tmA, &full[stage], c, t.row0);
-                        tma_load_3d(b_dst, second ? &tmB2 : &tmB, &full[stage], c, n0, t.e);
+                            for (int i = 0; i < 2; ++i) {
+                                tma_load_2d_pair(a_dst + i * kBBoxBytes, &tmA, bar, t.m0 + own + 64 * i, r);
+                                tma_load_2d_pair(b_dst + i * kBBoxBytes, &tmB, bar, n0 + 64 * i, r);
+                            }
+                        }
                     } else {
-                        tma_load_2d(a_dst, &tmA, &full[stage], kb * BK, t.row0);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (kTwoB)
-                                tma_load_3d(b_dst + i * kBBoxBytes, i < 2 ? &tmB : &tmB2, &full[stage],
-                                            n0 + 64 * (i & 1), kb * BK, t.e);
-                            else
-                                tma_load_3d(b_dst + i * kBBoxBytes, &tmB, &full[stage], n0 + 64 * i, kb * BK, t.e);
+                        if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
+                        if (FORM == FORM_GX) {
+                            const bool second = kb >= p.kblocks;
+                            const int c = (second ? kb - p.kblocks : kb) * BK;
+                            tma_load_2d_pair(a_dst, second ? &tmA2 : &tmA, bar, c, t.row0 + own);
+                            tma_load_3d_pair(b_dst, second ? &tmB2 : &tmB, bar, c, n0, t.e);
+                        } else {
+                            tma_load_2d_pair(a_dst, &tmA, bar, kb * BK, t.row0 + own);
+                            tma_load_3d_pair(b_dst, &tmB, bar, n0, kb * BK, t.e);
+                            tma_load_3d_pair(b_dst + kBBoxBytes, kTwoB ? &tmB2 : &tmB, bar, kTwoB ? n0 : n0 + 64, kb * BK,
+                                             t.e);
                         }
                     }
                     issued_mask |= 1u << stage;
@@ -274,218 +417,393 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            // no copy may still be landing in shared memory when the CTA exits
+            // the loads land before the MMAs that read them complete: wait for the last release of every stage
             for (int s = 0; s < kStages; ++s)
                 if ((issued_mask >> s) & 1u)
-                    if (!mbar_wait_bounded(&full[s], (issued_par >> s) & 1u, tmo)) give_up(SITE_GEMM_PRODUCER_DRAIN);
+                    if (!mbar_wait_bounded(&empty[s], (issued_par >> s) & 1u, tmo)) give_up(SITE_GEMM_PRODUCER_DRAIN);
         }
     } else if (warp == 1) {
-        // ---------------------------------------------------- MMA issuer
-        // the whole warp walks the tiles (it clears rows in GW); lane 0 issues
-        int stage = 0;
-        uint32_t phase = 0;
-        int acc = 0;
-        uint32_t acc_phase = 0;
-        bool stop = false;
-        constexpr bool kAMn = FORM == FORM_GW, kBMn = FORM != FORM_GX;
-        for (int tile = blockIdx.x; tile < total_tiles && !stop; tile += gridDim.x) {
-            const Tile t = decode<FORM>(tile, p, &tab);
-            const int kbs = tile_kblocks<FORM>(p, t);
-            if (kbs == 0) continue;  // GW, an expert without rows: the epilogue stores zeros by itself
-            const bool m64 = FORM != FORM_GW && t.rows <= BM / 2;
-            const uint32_t idesc =
-                m64 ? make_idesc_majors(BM / 2, BN_MMA, kAMn, kBMn) : make_idesc_majors(BM, BN_MMA, kAMn, kBMn);
-            bool ok = mbar_wait_bounded(&tempty[acc], acc_phase ^ 1u, tmo);
-            if (!__all_sync(0xffffffffu, ok)) {
-                if (lane == 0) give_up(SITE_GEMM_MMA_TMEM_EMPTY);
-                break;
-            }
-            tc_fence_after();
-            const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN_MMA);
-            for (int kb = 0; kb < kbs; ++kb) {
-                if (__shfl_sync(0xffffffffu, *abort_flag, 0)) { stop = true; break; }
-                ok = mbar_wait_bounded(&full[stage], phase, tmo);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    if (lane == 0) give_up(SITE_GEMM_MMA_FULL);
-                    stop = true;
-                    break;
-                }
-                uint8_t* a_st = sA + stage * kAStageBytes;
-                uint8_t* b_st = sB + stage * kBStageBytes;
-                int steps = BK / 16;
-                if (FORM == FORM_GW) {
-                    const int held = t.rows - kb * BK;
-                    if (held < BK) {
-                        steps = (held + 15) / 16;
-                        // rows [held, 16 steps) of the six boxes: 128 bytes each
-                        const int nz = (16 * steps - held) * 8;
-                        for (int i = lane; i < nz; i += 32) {
-                            const int off = held * 128 + i * 16;
-#pragma unroll
-                            for (int b = 0; b < 6; ++b)
-                                *reinterpret_cast<uint4*>((b < 2 ? a_st + b * kBBoxBytes : b_st + (b - 2) * kBBoxBytes) +
-                                                          off) = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                }
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t a_addr = smem_u32(a_st), b_addr = smem_u32(b_st);
-                    for (int kk = 0; kk < steps; ++kk) {
-                        // contraction-major: +32 bytes per K=16 step inside the 128-byte swizzle row;
-                        // output-major: +16 rows of 128 bytes per step, 64-column boxes 8 KB apart
-                        const uint64_t adesc = kAMn ? smem_desc_sw128(a_addr + kk * 2048, kBBoxBytes, 1024)
-                                                    : smem_desc_sw128(a_addr + kk * 32, 16, 1024);
-                        const uint64_t bdesc = kBMn ? smem_desc_sw128(b_addr + kk * 2048, kBBoxBytes, 1024)
-                                                    : smem_desc_sw128(b_addr + kk * 32, 16, 1024);
-                        tc_mma_f16(d_tmem, adesc, bdesc, idesc, (kb | kk) != 0 ? 1u : 0u);
-                    }
-                    tc_commit(&empty[stage]);
-                }
-                __syncwarp();
-                if (++stage == kStages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
-            if (stop) break;
-            if (lane == 0) tc_commit(&tfull[acc]);
-            acc ^= 1;
-            if (acc == 0) acc_phase ^= 1u;
-        }
-        // every MMA issued by this thread has completed before TMEM is freed
         if (lane == 0) {
-            tc_commit(drain);
+            if (rank == 0) {
+                // -------------------------------------------- MMA issuer (leader)
+                // Its loop is kept short: with warp-wide votes and an abort check in every block, 236 of a
+                // block's 695 clocks passed between the MMAs (512 of work).
+                int stage = 0, place = 0, acc = 0;
+                uint32_t full_par = 0, ready_par = 0;  // parity of each stage's next use of that barrier
+                uint32_t acc_phase = 0;
+                bool stop = false;
+                constexpr bool kAMn = kGw, kBMn = FORM != FORM_GX;
+                // blocks of 64 that one accumulator sums: all, or (GW, fp32 output) a run
+                constexpr int kRun = kGw && EPI == EPI_F32 ? kRunRows / BK : 1 << 30;
+                // contraction-major: +32 bytes per K=16 step inside the 128-byte swizzle row;
+                // output-major: +16 rows of 128 bytes per step, 64-column boxes 8 KB apart
+                const uint64_t a_desc0 = smem_desc_sw128(smem_u32(sA), kAMn ? kBBoxBytes : 16, 1024);
+                const uint64_t b_desc0 = smem_desc_sw128(smem_u32(sB), kBMn ? kBBoxBytes : 16, 1024);
+                constexpr uint32_t kAStep = (kAMn ? 2048 : 32) >> 4, kBStep = (kBMn ? 2048 : 32) >> 4;
+                for (int tile = pair; tile < total_tiles && !stop; tile += npairs) {
+                    if (*abort_flag) break;
+                    const Tile t = decode<FORM>(tile, p, &tab, place);
+                    const int kbs = tile_kblocks<FORM>(p, t);
+                    if (kbs == 0) continue;  // GW, an expert without rows: the epilogue stores zeros by itself
+                    const uint32_t idesc = t.half ? make_idesc_majors(BM / 2, BN_MMA, kAMn, kBMn)
+                                                  : make_idesc_majors(BM, BN_MMA, kAMn, kBMn);
+                    for (int kb = 0; kb < kbs; ++kb) {
+                        const int kr = kb % kRun;  // block of this run
+                        if (kr == 0) {             // a new accumulator
+                            if (kb > 0) {
+                                tc_commit_pair_mc(&tfull[acc], 0x3);
+                                acc ^= 1;
+                                if (acc == 0) acc_phase ^= 1u;
+                            }
+                            if (!mbar_wait_bounded(&tempty[acc], acc_phase ^ 1u, tmo)) {
+                                give_up(SITE_GEMM_MMA_TMEM_EMPTY);
+                                stop = true;
+                                break;
+                            }
+                        }
+                        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN_MMA);
+                        int steps = BK / 16;
+                        bool ok;
+                        if (kGw && t.rows - kb * BK < BK) {
+                            steps = (t.rows - kb * BK + 15) / 16;
+                            ok = mbar_wait_bounded_cluster(&ready[stage], (ready_par >> stage) & 1u, tmo);
+                            ready_par ^= 1u << stage;
+                        } else {
+                            ok = mbar_wait_bounded(&full[stage], (full_par >> stage) & 1u, tmo);
+                            full_par ^= 1u << stage;
+                        }
+                        if (!ok) {
+                            give_up(SITE_GEMM_MMA_FULL);
+                            stop = true;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t a0 = a_desc0 + (uint32_t)stage * (kABytes >> 4);
+                        const uint64_t b0 = b_desc0 + (uint32_t)stage * (kBBytes >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < BK / 16; ++kk)
+                            if (!kGw || kk < steps)
+                                tc_mma_f16_pair(d_tmem, a0 + kk * kAStep, b0 + kk * kBStep, idesc,
+                                                (kr | kk) != 0 ? 1u : 0u);
+                        tc_commit_pair_mc(&empty[stage], 0x3);
+                        if (++stage == kStages) stage = 0;
+                    }
+                    if (stop) break;
+                    tc_commit_pair_mc(&tfull[acc], 0x3);
+                    acc ^= 1;
+                    if (acc == 0) acc_phase ^= 1u;
+                }
+                // every pair MMA has completed before either CTA frees its TMEM
+                tc_commit_pair_mc(drain, 0x3);
+            }
             if (!mbar_wait_bounded(drain, 0, tmo)) give_up(SITE_GEMM_DRAIN);
         }
+        __syncwarp();
+    } else if (warp == kClearWarp) {
+        // ---------------------------------------------------- clearing (GW, both CTAs)
+        if (kGw) {
+            int stage = 0, place = 0;
+            uint32_t tail_par = 0;  // parity of each stage's next tail
+            for (int tile = pair; tile < total_tiles; tile += npairs) {
+                if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
+                const Tile t = decode<FORM>(tile, p, &tab, place);
+                const int kbs = tile_kblocks<FORM>(p, t);
+                const int held = t.rows % BK;
+                if (held != 0) {
+                    const int st = (stage + kbs - 1) % kStages;
+                    const bool ok = mbar_wait_bounded(&tail[st], (tail_par >> st) & 1u, tmo);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        if (lane == 0) give_up(SITE_GROUPED_TAIL);
+                        break;
+                    }
+                    tail_par ^= 1u << st;
+                    // rows [held, next multiple of 16) of this CTA's four boxes, 128 bytes each
+                    const int n = ((held + 15) / 16 * 16 - held) * 8;
+                    uint8_t* a = sA + st * kABytes + held * 128;
+                    uint8_t* b = sB + st * kBBytes + held * 128;
+                    for (int i = lane; i < n; i += 32)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            *reinterpret_cast<uint4*>(a + x * kBBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4*>(b + x * kBBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(ready_lead + 8u * st);
+                }
+                stage = (stage + kbs) % kStages;
+            }
+        }
     } else {
-        // ---------------------------------------------------- epilogue
-        const int q = warp & 3;  // TMEM lanes 32q..32q+31 are reachable from this warp
-        int acc = 0;
+        // ---------------------------------------------------- epilogue (both CTAs)
+        const int q = warp & 3;            // TMEM lanes 32q..32q+31 are reachable from this warp
+        const int hc = (warp - 2) >> 2;    // which half of the columns it takes
+        uint8_t* slabs = smem + S::kSlabOff + (warp - 2) * S::kSlabs * kSlabBytes;
+        int acc = 0, place = 0, turn = 0;
         uint32_t acc_phase = 0;
-        for (int tile = blockIdx.x; tile < total_tiles; tile += gridDim.x) {
+        // the next accumulator, complete; false: gave up
+        auto acquire = [&]() -> bool {
+            const bool ok = mbar_wait_bounded(&tfull[acc], acc_phase, tmo);
+            if (!__all_sync(0xffffffffu, ok)) {
+                if (lane == 0) give_up(SITE_GEMM_EPI_TMEM_FULL);
+                return false;
+            }
+            tc_fence_after();
+            return true;
+        };
+        auto release = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty_lead + 8u * acc);
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        };
+        // a slab that no earlier store still reads
+        auto next_slab = [&]() -> uint8_t* {
+            if (lane == 0) tma_store_wait_read<S::kSlabs - 1>();
+            __syncwarp();
+            uint8_t* slab = slabs + turn * kSlabBytes;
+            turn = (turn + 1) % S::kSlabs;
+            return slab;
+        };
+        for (int tile = pair; tile < total_tiles; tile += npairs) {
             const int ab = __shfl_sync(0xffffffffu, *abort_flag, 0);
             if (ab) break;
-            const Tile t = decode<FORM>(tile, p, &tab);
-            const int n0 = t.nt * p.bn_out;
-            const bool none = tile_kblocks<FORM>(p, t) == 0;
-            if (!none) {
-                const bool ok = mbar_wait_bounded(&tfull[acc], acc_phase, tmo);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    if (lane == 0) give_up(SITE_GEMM_EPI_TMEM_FULL);
-                    break;
-                }
-                tc_fence_after();
-            }
-            // M=128: row 32q + lane.  M=64: rows 16q..16q+15 sit in lanes 0-15 of this warp's quarter
-            const bool m64 = FORM != FORM_GW && t.rows <= BM / 2;
-            const int r = m64 ? 16 * q + lane : q * 32 + lane;
-            const bool valid = FORM == FORM_GW ? t.m0 + r < p.M : r < t.rows && (!m64 || lane < 16);
-            const int64_t orow = FORM == FORM_GW ? (int64_t)t.e * p.M + t.m0 + (valid ? r : 0) : t.row0 + (valid ? r : 0);
-            const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN_MMA);
-            if (EPI == EPI_SWIGLU_GRAD) {
-                for (int c = 0; c < 128; c += 16) {
-                    uint32_t g[16], u[16];
-                    tmem_ld_16(tbase + c, g);
-                    tmem_ld_16(tbase + 128 + c, u);
-                    const int col = n0 + c;
-                    float d[16];
-                    if (valid && col < p.N) {
+            const Tile t = decode<FORM>(tile, p, &tab, place);
+            // full tile: rows 32q.. of this CTA's 128, TMEM columns [128 hc, +128); half tile: rows 32 (q & 1)..
+            // of its 64, output columns from 128 (q >> 1), TMEM columns [64 hc, +64)
+            const int r0 = t.half ? 64 * rank + 32 * (q & 1) : 128 * rank + 32 * q;
+            const int rn = min(32, (kGw ? p.M - t.m0 : t.rows) - r0);  // rows of this warp (none: <= 0)
+            const int row = (kGw ? t.m0 : t.row0) + r0;                // the first of them (GW: of the expert's matrix)
+            const int64_t first = kGw ? (int64_t)t.e * p.M + row : row;
+            const int tc0 = t.half ? 64 * hc : 128 * hc;               // its TMEM columns
+            const int ncols = t.half ? 64 : 128;
+            // output column of TMEM column tc0 (SwiGLU: of output tc0 / 2, see below)
+            const int col0 = t.nt * p.bn_out + (t.half ? 128 * (q >> 1) : 0) + tc0;
+            // row r of this warp at column col of a [.., N] tensor
+            auto at_col = [&](auto* base, int col) {
+                return [=](int r) { return r < rn ? base + (first + r) * p.N + col : nullptr; };
+            };
+            const uint32_t tq = tmem_base + ((uint32_t)(q * 32) << 16) + tc0;
+            if (kGw && EPI == EPI_F32) {
+                // runs of kRunRows rows are summed in TMEM and the runs in registers (round to nearest): the
+                // tensor cores' own fp32 sums lose about 2e-8 of the value with each step of 16
+                float x[128];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            *reinterpret_cast<float4*>(d + 4 * i) =
-                                *reinterpret_cast<const float4*>(p.dh + orow * p.N + col + 4 * i);
+                for (int i = 0; i < 128; ++i) x[i] = 0.f;
+                const int runs = (tile_kblocks<FORM>(p, t) * BK + kRunRows - 1) / kRunRows;
+                bool ok = true;
+#pragma unroll 1
+                for (int run = 0; run < runs && ok; ++run) {
+                    ok = acquire();
+                    const uint32_t tb = tq + (uint32_t)(acc * BN_MMA);
+#pragma unroll
+                    for (int c = 0; c < 128; c += 16) {
+                        if (c >= ncols) break;
+                        uint32_t v[16];
+                        tmem_ld_16(tb + c, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[c + i] += __uint_as_float(v[i]);
                     }
-                    tmem_ld_wait();
-                    if (valid && col < p.N) {
-                        float h[16], dg[16], du[16];
+                    release();
+                }
+                if (!ok) break;
+                if (rn <= 0 || (runs == 0 && p.accumulate)) continue;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            swiglu_grad(__uint_as_float(g[i]), __uint_as_float(u[i]), d[i], h[i], dg[i], du[i]);
-                        store16_bf16(p.h + orow * p.N, col, p.N, h);
-                        store16_bf16(p.d0 + orow * p.N, col, p.N, dg);
-                        store16_bf16(p.d1 + orow * p.N, col, p.N, du);
+                for (int c = 0; c < 128; c += 32) {
+                    if (c >= ncols || col0 + c >= p.N) break;
+                    uint8_t* slab = next_slab();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) *slab_piece(slab, lane, j) = pack4_f32(x + c + 4 * j);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (p.accumulate)
+                            tma_store<true, true>(&tmO, slab, col0 + c, row, t.e);
+                        else
+                            tma_store<true, false>(&tmO, slab, col0 + c, row, t.e);
+                    }
+                }
+                continue;
+            }
+            const bool none = tile_kblocks<FORM>(p, t) == 0;  // GW, an expert without rows
+            // what the epilogue reads from memory is fetched before the accumulator is waited for
+            constexpr bool kGrad = EPI == EPI_SWIGLU_GRAD || EPI == EPI_GELU_GRAD;
+            constexpr bool kFetch = kGrad || (kGw && EPI == EPI_BF16);
+            // SwiGLU: each CTA's 128 columns are [gate 64 | up 64] of the same 64 outputs; a warp takes the
+            // 64 outputs of its half (full tile) or 32 of them (half tile)
+            const int gcol0 = t.nt * 128 + (t.half ? 64 * (q >> 1) + 32 * hc : 64 * hc);
+            uint4 seen[kFetch ? 2 : 1][8];
+            if (kGw && EPI == EPI_BF16) {
+                if (p.accumulate && !none) {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const int col = col0 + 64 * s;
+                        fetch_rows<__nv_bfloat16>(seen[s], lane, 64 * s < ncols ? p.N - col : 0,
+                                                  at_col(static_cast<const __nv_bfloat16*>(p.out), col));
+                    }
+                }
+            }
+            if (kGrad) {
+                const int g0 = EPI == EPI_SWIGLU_GRAD ? gcol0 : col0;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) fetch_rows<float>(seen[s], lane, p.N - (g0 + 32 * s), at_col(p.dh, g0 + 32 * s));
+            }
+            if (!none && !acquire()) break;
+            const uint32_t tb = tq + (uint32_t)(acc * BN_MMA);
+            // fp32 accumulators of 32 columns
+            auto load32 = [&](uint32_t taddr, float* x) {
+                uint32_t v[2][16];
+                tmem_ld_16(taddr, v[0]);
+                tmem_ld_16(taddr + 16, v[1]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i >> 4][i & 15]);
+            };
+            if (kGrad) {
+                // dh comes in and h, the gradients go out through the slab, 32 columns at a time
+                const int n = EPI == EPI_SWIGLU_GRAD ? ncols / 2 : ncols;
+                const uint32_t ta = EPI == EPI_SWIGLU_GRAD && t.half ? tb - tc0 + 32 * hc : tb;
+                const int g0 = EPI == EPI_SWIGLU_GRAD ? gcol0 : col0;
+                uint8_t* slab = slabs;
+#pragma unroll
+                for (int c = 0; c < (EPI == EPI_SWIGLU_GRAD ? 64 : 128); c += 32) {
+                    const int col = g0 + c;
+                    if (c >= n || col >= p.N) break;
+                    put_rows(slab, lane, seen[c / 32 & 1]);
+                    float a[32], u[32], d[32], h[32];
+                    load32(ta + c, a);
+                    if (EPI == EPI_SWIGLU_GRAD) load32(ta + 64 + c, u);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(d + 4 * j) = *slab_piece(slab, lane, j);
+                    if (EPI == EPI_GELU_GRAD) {
+                        if (c < 64) fetch_rows<float>(seen[c / 32 & 1], lane, c + 64 < n ? p.N - (col + 64) : 0, at_col(p.dh, col + 64));
+                        add16_bf16(p.bias + (int64_t)t.e * p.N, col, p.N, a);
+                        add16_bf16(p.bias + (int64_t)t.e * p.N, col + 16, p.N, a + 16);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        if (EPI == EPI_SWIGLU_GRAD)
+                            swiglu_grad(a[i], u[i], d[i], h[i], a[i], u[i]);
+                        else
+                            gelu_grad(a[i], d[i], h[i], a[i]);
+                    }
+                    // pieces 0-3: h, 4-7: the gradient; then the gradient of up
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        *slab_piece(slab, lane, j) = pack8_bf16(h + 8 * j);
+                        *slab_piece(slab, lane, j + 4) = pack8_bf16(a + 8 * j);
+                    }
+                    auto h_row = at_col(p.h, col), g_row = at_col(p.d0, col - 32);
+                    store_slab<__nv_bfloat16>(slab, lane, 64, [&](int r) { return (lane & 7) < 4 ? h_row(r) : g_row(r); });
+                    if (EPI == EPI_SWIGLU_GRAD) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) *slab_piece(slab, lane, j) = pack8_bf16(u + 8 * j);
+                        store_slab<__nv_bfloat16>(slab, lane, 32, at_col(p.d1, col));
                     }
                 }
             } else {
-                for (int c = 0; c < BN_MMA; c += 16) {
-                    uint32_t v[16];
-                    if (!none) {
-                        tmem_ld_16(tbase + c, v);
-                        tmem_ld_wait();
-                    } else {
+                constexpr int kCols = EPI == EPI_F32 ? 32 : 64;  // columns of a slab
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = 0u;
+                for (int c = 0; c < 128; c += kCols) {
+                    const int col = col0 + c;
+                    if (c >= ncols || col >= p.N || rn <= 0 || (none && p.accumulate)) break;
+                    float x[kCols];
+                    if (none) {
+#pragma unroll
+                        for (int i = 0; i < kCols; ++i) x[i] = 0.f;
+                    } else {
+                        load32(tb + c, x);
+                        if (kCols == 64) load32(tb + c + 32, x + 32);
                     }
-                    const int col = n0 + c;
-                    if (!valid || col >= p.N || (none && p.accumulate)) continue;
-                    float x[16];
+                    uint8_t* slab = next_slab();
+                    if (FORM == FORM_FWD && p.bias != nullptr) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[i]);
-                    if (FORM == FORM_FWD && p.bias != nullptr) add16_bf16(p.bias + (int64_t)t.e * p.N, col, p.N, x);
-                    if (EPI == EPI_GELU_GRAD) {
-                        float h[16], dp[16];
+                        for (int i = 0; i < kCols; i += 16) add16_bf16(p.bias + (int64_t)t.e * p.N, col + i, p.N, x + i);
+                    }
+                    if (EPI == EPI_F32) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float4 d = *reinterpret_cast<const float4*>(p.dh + orow * p.N + col + 4 * i);
-                            gelu_grad(x[4 * i], d.x, h[4 * i], dp[4 * i]);
-                            gelu_grad(x[4 * i + 1], d.y, h[4 * i + 1], dp[4 * i + 1]);
-                            gelu_grad(x[4 * i + 2], d.z, h[4 * i + 2], dp[4 * i + 2]);
-                            gelu_grad(x[4 * i + 3], d.w, h[4 * i + 3], dp[4 * i + 3]);
-                        }
-                        store16_bf16(p.h + orow * p.N, col, p.N, h);
-                        store16_bf16(p.d0 + orow * p.N, col, p.N, dp);
-                    } else if (EPI == EPI_F32) {
-                        float* dst = static_cast<float*>(p.out) + orow * p.N + col;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (col + 4 * i < p.N) {
-                                float4 w = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-                                if (FORM == FORM_GW && p.accumulate) {
-                                    const float4 old = *reinterpret_cast<const float4*>(dst + 4 * i);
-                                    w.x += old.x;
-                                    w.y += old.y;
-                                    w.z += old.z;
-                                    w.w += old.w;
-                                }
-                                *reinterpret_cast<float4*>(dst + 4 * i) = w;
-                            }
+                        for (int j = 0; j < 8; ++j) *slab_piece(slab, lane, j) = pack4_f32(x + 4 * j);
                     } else {
-                        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + orow * p.N;
-                        if (FORM == FORM_GW && p.accumulate) add16_bf16(dst, col, p.N, x);
-                        store16_bf16(dst, col, p.N, x);
+                        if (kGw && p.accumulate) {
+                            // what is there, through the slab; added in fp32, one rounding
+                            put_rows(slab, lane, seen[c / 64 & 1]);
+#pragma unroll
+                            for (int j = 0; j < kCols / 8; ++j) {
+                                const uint4 v = *slab_piece(slab, lane, j);
+                                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    x[8 * j + 2 * i] += bf16_lo(w[i]);
+                                    x[8 * j + 2 * i + 1] += bf16_hi(w[i]);
+                                }
+                            }
+                            __syncwarp();
+                        }
+#pragma unroll
+                        for (int j = 0; j < kCols / 8; ++j) *slab_piece(slab, lane, j) = pack8_bf16(x + 8 * j);
+                    }
+                    using Out = typename std::conditional<EPI == EPI_F32, float, __nv_bfloat16>::type;
+                    if (kGw || rn == 32) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) tma_store<kGw, false>(&tmO, slab, col, row, t.e);
+                    } else {
+                        store_slab<Out>(slab, lane, p.N - col, at_col(static_cast<Out*>(p.out), col));
+                        // an empty group, so that the groups count the slabs' uses
+                        if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     }
                 }
             }
-            if (!none) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&tempty[acc]);
-                acc ^= 1;
-                if (acc == 0) acc_phase ^= 1u;
-            }
+            if (!none) release();
         }
+        if (lane == 0) tma_store_wait_all();
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync_all();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, kTmemCols);
+        tmem_dealloc_pair(tmem_base, kTmemCols);
     }
 }
 
 // ------------------------------------------------------------------ host side
 template <int FORM, int EPI>
 cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2, const CUtensorMap& b2,
-                   const GroupedParams& p, int64_t tiles_upper, cudaStream_t s) {
-    static std::atomic<bool> attr_set[64];
-    const cudaError_t err = ensure_smem_attr(attr_set, grouped_kernel<FORM, EPI>, kSmemBytes);
-    if (err != cudaSuccess) return err;
-    const int grid = (int)min64(tiles_upper, (int64_t)sm_count());
-    if (grid <= 0) return cudaSuccess;
-    return launch_kernel(grouped_kernel<FORM, EPI>, dim3(grid), dim3(kThreads), kSmemBytes, s, a, b, a2, b2, p);
+                   const CUtensorMap& o, const GroupedParams& p, int64_t tiles_upper, cudaStream_t s) {
+    static std::atomic<int> max_pairs[64];  // resident clusters per device, 0 until measured
+    int dev = 0;
+    cudaGetDevice(&dev);
+    int pairs_cap = dev < 64 ? max_pairs[dev].load(std::memory_order_acquire) : 0;
+    if (pairs_cap <= 0) {
+        cudaError_t err = cudaFuncSetAttribute(grouped_kernel<FORM, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Smem<EPI>::kBytes);
+        if (err != cudaSuccess) return err;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * (unsigned)(sm_count() / 2));
+        cfg.blockDim = dim3(kThreadsG);
+        cfg.dynamicSmemBytes = Smem<EPI>::kBytes;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2;
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        err = cudaOccupancyMaxActiveClusters(&n, grouped_kernel<FORM, EPI>, &cfg);
+        if (err != cudaSuccess || n <= 0) n = sm_count() / 2;
+        pairs_cap = n;
+        if (dev < 64) max_pairs[dev].store(n, std::memory_order_release);
+    }
+    const int pairs = (int)min64(tiles_upper, (int64_t)pairs_cap);
+    if (pairs <= 0) return cudaSuccess;
+    return launch_kernel(grouped_kernel<FORM, EPI>, dim3(2 * pairs), dim3(kThreadsG), Smem<EPI>::kBytes, s, a, b, a2, b2,
+                         o, p);
 }
 
 // Activations [rows, cols], boxes [box_rows, 64].
@@ -507,14 +825,18 @@ int64_t row_tiles_upper(const GroupedArgs& a) { return a.rows / BM + a.E; }
 }  // namespace
 
 cudaError_t launch_grouped_fwd_bf16(const GroupedArgs& a, cudaStream_t s) {
-    CUtensorMap mA, mB, mB2;
-    bool ok = act_map(&mA, a.x, a.rows, a.K, 128);
-    ok = ok && make_map_3d(&mB, a.w, a.E, a.K, a.N, 64, BK);
+    CUtensorMap mA, mB, mB2, mO;
     const bool two = a.grad_act == GRAD_SWIGLU;
+    bool ok = act_map(&mA, a.x, a.rows, a.K, 128);
+    ok = ok && make_map_3d(&mB, a.w, a.E, a.K, a.N, false, 64, BK);
     if (two)
-        ok = ok && make_map_3d(&mB2, a.w2, a.E, a.K, a.N, 64, BK);
+        ok = ok && make_map_3d(&mB2, a.w2, a.E, a.K, a.N, false, 64, BK);
     else
         mB2 = mB;
+    if (a.grad_act == GRAD_NONE)
+        ok = ok && act_map(&mO, a.y, a.rows, a.N, 32);
+    else
+        mO = mA;  // three outputs, stored by the warps
     if (!ok) return cudaErrorInvalidValue;
     GroupedParams p = params(a);
     p.N = a.N;
@@ -528,22 +850,23 @@ cudaError_t launch_grouped_fwd_bf16(const GroupedArgs& a, cudaStream_t s) {
     p.d0 = static_cast<__nv_bfloat16*>(a.d0);
     p.d1 = static_cast<__nv_bfloat16*>(a.d1);
     const int64_t tiles = row_tiles_upper(a) * p.n_tiles;
-    if (two) return launch<FORM_FWD, EPI_SWIGLU_GRAD>(mA, mB, mA, mB2, p, tiles, s);
-    if (a.grad_act == GRAD_GELU) return launch<FORM_FWD, EPI_GELU_GRAD>(mA, mB, mA, mB2, p, tiles, s);
-    return launch<FORM_FWD, EPI_BF16>(mA, mB, mA, mB2, p, tiles, s);
+    if (two) return launch<FORM_FWD, EPI_SWIGLU_GRAD>(mA, mB, mA, mB2, mO, p, tiles, s);
+    if (a.grad_act == GRAD_GELU) return launch<FORM_FWD, EPI_GELU_GRAD>(mA, mB, mA, mB2, mO, p, tiles, s);
+    return launch<FORM_FWD, EPI_BF16>(mA, mB, mA, mB2, mO, p, tiles, s);
 }
 
 cudaError_t launch_grouped_gx_bf16(const GroupedArgs& a, cudaStream_t s) {
-    CUtensorMap mA, mB, mA2, mB2;
+    CUtensorMap mA, mB, mA2, mB2, mO;
     bool ok = act_map(&mA, a.dy, a.rows, a.N, 128);
-    ok = ok && make_map_3d(&mB, a.w, a.E, a.K, a.N, 64, 256);
+    ok = ok && make_map_3d(&mB, a.w, a.E, a.K, a.N, false, 64, 128);
     if (a.dy2 != nullptr) {
         ok = ok && act_map(&mA2, a.dy2, a.rows, a.N, 128);
-        ok = ok && make_map_3d(&mB2, a.w2, a.E, a.K, a.N, 64, 256);
+        ok = ok && make_map_3d(&mB2, a.w2, a.E, a.K, a.N, false, 64, 128);
     } else {
         mA2 = mA;
         mB2 = mB;
     }
+    ok = ok && (a.out_f32 ? make_map_2d_f32(&mO, a.dx, a.rows, a.K, 32, 32) : act_map(&mO, a.dx, a.rows, a.K, 32));
     if (!ok) return cudaErrorInvalidValue;
     GroupedParams p = params(a);
     p.N = a.K;
@@ -552,14 +875,15 @@ cudaError_t launch_grouped_gx_bf16(const GroupedArgs& a, cudaStream_t s) {
     p.n_tiles = (a.K + 255) / 256;
     p.out = a.dx;
     const int64_t tiles = row_tiles_upper(a) * p.n_tiles;
-    return a.out_f32 ? launch<FORM_GX, EPI_F32>(mA, mB, mA2, mB2, p, tiles, s)
-                     : launch<FORM_GX, EPI_BF16>(mA, mB, mA2, mB2, p, tiles, s);
+    return a.out_f32 ? launch<FORM_GX, EPI_F32>(mA, mB, mA2, mB2, mO, p, tiles, s)
+                     : launch<FORM_GX, EPI_BF16>(mA, mB, mA2, mB2, mO, p, tiles, s);
 }
 
 cudaError_t launch_grouped_gw_bf16(const GroupedArgs& a, cudaStream_t s) {
-    CUtensorMap mA, mB;
+    CUtensorMap mA, mB, mO;
     bool ok = act_map(&mA, a.x, a.rows, a.K, BK);
     ok = ok && act_map(&mB, a.dy, a.rows, a.N, BK);
+    ok = ok && make_map_3d(&mO, a.dw, a.E, a.K, a.N, a.out_f32, a.out_f32 ? 32 : 64, 32);
     if (!ok) return cudaErrorInvalidValue;
     GroupedParams p = params(a);
     p.M = a.K;
@@ -569,8 +893,8 @@ cudaError_t launch_grouped_gw_bf16(const GroupedArgs& a, cudaStream_t s) {
     p.out = a.dw;
     p.accumulate = a.accumulate ? 1 : 0;
     const int64_t tiles = (int64_t)a.E * p.m_tiles * p.n_tiles;
-    return a.out_f32 ? launch<FORM_GW, EPI_F32>(mA, mB, mA, mB, p, tiles, s)
-                     : launch<FORM_GW, EPI_BF16>(mA, mB, mA, mB, p, tiles, s);
+    return a.out_f32 ? launch<FORM_GW, EPI_F32>(mA, mB, mA, mB, mO, p, tiles, s)
+                     : launch<FORM_GW, EPI_BF16>(mA, mB, mA, mB, mO, p, tiles, s);
 }
 
 }  // namespace moe
