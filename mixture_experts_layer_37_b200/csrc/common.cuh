@@ -52,6 +52,7 @@ enum WaitSite : uint32_t {
     SITE_EP_COMBINE_ROW = 0x303,
     SITE_GROUPED_OFFSETS = 0x501,
     SITE_GROUPED_TAIL = 0x502,
+    SITE_GROUPED_OLD = 0x503,
 };
 
 __host__ __device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }

@@ -47,8 +47,7 @@
 // and 64-127 for the others.
 //
 // Stores go through shared memory: a warp's 32 rows of 128 bytes, then one TMA
-// store (or fp32 reduction, when accumulating), or, for a warp with fewer rows,
-// whole lines by eight lanes per row.  (Lanes storing their own rows 16 bytes
+// store, or, for a warp with fewer rows, whole lines by eight lanes per row.  (Lanes storing their own rows 16 bytes
 // at a time moved three times the sectors.)
 // Every wait is bounded in time, as in the other kernels.
 #include <type_traits>
@@ -85,7 +84,7 @@ struct Smem {
     static constexpr int kStages = EPI == EPI_F32 ? 5 : 6;
     static constexpr int kSlabOff = kStages * kStageBytes;
     static constexpr int kBarOff = kSlabOff + kEpiWarps * kSlabs * kSlabBytes;
-    static constexpr int kBytes = kBarOff + 256 + 1024 /*alignment*/;
+    static constexpr int kBytes = kBarOff + 384 + 1024 /*alignment*/;
 };
 
 struct GroupedParams {
@@ -111,7 +110,16 @@ constexpr uint32_t make_idesc_majors(int m, int n, bool a_mn, bool b_mn) {
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// tma_load_2d_pair with three coordinates.
+// tma_load_2d and tma_load_2d_pair with three coordinates.
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const void* map, uint64_t* bar, int32_t c0, int32_t c1,
+                                            int32_t c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
 __device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const void* map, uint32_t bar_cluster_addr, int32_t c0,
                                                  int32_t c1, int32_t c2) {
     asm volatile(
@@ -207,17 +215,13 @@ __device__ __forceinline__ void put_rows(uint8_t* slab, int lane, const uint4 (&
     __syncwarp();
 }
 
-// A slab by TMA: to [.., col..] of row `row` (of expert e where the tensor has
-// three dimensions), or added to it (fp32).  One lane.
-template <bool THREE, bool ADD>
+// A slab by TMA to [.., col..] of row `row` (of expert e where the tensor has
+// three dimensions).  One lane.
+template <bool THREE>
 __device__ __forceinline__ void tma_store(const void* map, const uint8_t* slab, int col, int row, int e) {
     const uint64_t m = reinterpret_cast<uint64_t>(map);
     const uint32_t sa = smem_u32(slab);
-    if (THREE && ADD)
-        asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(m),
-                     "r"(sa), "r"(col), "r"(row), "r"(e)
-                     : "memory");
-    else if (THREE)
+    if (THREE)
         asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(m),
                      "r"(sa), "r"(col), "r"(row), "r"(e)
                      : "memory");
@@ -307,7 +311,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
     uint64_t* drain = tempty + 2;
     uint64_t* tail = drain + 1;  // [stage] GW: this CTA's part of an expert's last, partly filled block
     uint64_t* ready = tail + kStages;  // [stage] GW, leader: both CTAs have cleared such a block
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ready + kStages);
+    uint64_t* olds = ready + kStages;  // [epilogue warp][2] GW, fp32: what is there, in the warp's slabs
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(olds + 2 * kEpiWarps);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     __shared__ GroupTables tab;
 
@@ -326,6 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
         mbar_init(&tempty[0], 2 * kEpiWarps);
         mbar_init(&tempty[1], 2 * kEpiWarps);
         mbar_init(drain, 1);
+        for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(&olds[i], 1);
         *abort_flag = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
@@ -539,8 +545,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
         const int q = warp & 3;            // TMEM lanes 32q..32q+31 are reachable from this warp
         const int hc = (warp - 2) >> 2;    // which half of the columns it takes
         uint8_t* slabs = smem + S::kSlabOff + (warp - 2) * S::kSlabs * kSlabBytes;
+        uint64_t* old = olds + 2 * (warp - 2);
         int acc = 0, place = 0, turn = 0;
-        uint32_t acc_phase = 0;
+        uint32_t acc_phase = 0, old_par = 0;
         // the next accumulator, complete; false: gave up
         auto acquire = [&]() -> bool {
             const bool ok = mbar_wait_bounded(&tfull[acc], acc_phase, tmo);
@@ -591,6 +598,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
                 float x[128];
 #pragma unroll
                 for (int i = 0; i < 128; ++i) x[i] = 0.f;
+                if (p.accumulate && rn > 0 && t.rows > 0) {
+                    // accumulating: what is there, loaded while the products run, slab by slab
+                    if (lane == 0) {
+                        tma_store_wait_read<0>();
+#pragma unroll
+                        for (int s = 0; s < 2; ++s)
+                            if (col0 + 32 * s < p.N) {
+                                mbar_arrive_expect_tx(&old[s], kSlabBytes);
+                                tma_load_3d(slabs + s * kSlabBytes, &tmO, &old[s], col0 + 32 * s, row, t.e);
+                            }
+                    }
+                    __syncwarp();
+                    bool in = true;
+#pragma unroll
+                    for (int c = 0; c < 128; c += 32) {
+                        const int s = c / 32 & 1;
+                        if (c >= ncols || col0 + c >= p.N || !in) break;
+                        in = __all_sync(0xffffffffu, mbar_wait_bounded(&old[s], (old_par >> s) & 1u, tmo));
+                        old_par ^= 1u << s;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(x + c + 4 * j) =
+                            *slab_piece(slabs + s * kSlabBytes, lane, j);
+                        __syncwarp();
+                        if (lane == 0 && in && c + 64 < ncols && col0 + c + 64 < p.N) {
+                            mbar_arrive_expect_tx(&old[s], kSlabBytes);
+                            tma_load_3d(slabs + s * kSlabBytes, &tmO, &old[s], col0 + c + 64, row, t.e);
+                        }
+                    }
+                    if (!in) {
+                        if (lane == 0) give_up(SITE_GROUPED_OLD);
+                        break;
+                    }
+                }
                 const int runs = (tile_kblocks<FORM>(p, t) * BK + kRunRows - 1) / kRunRows;
                 bool ok = true;
 #pragma unroll 1
@@ -619,10 +659,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        if (p.accumulate)
-                            tma_store<true, true>(&tmO, slab, col0 + c, row, t.e);
-                        else
-                            tma_store<true, false>(&tmO, slab, col0 + c, row, t.e);
+                        tma_store<true>(&tmO, slab, col0 + c, row, t.e);
                     }
                 }
                 continue;
@@ -749,7 +786,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
                     if (kGw || rn == 32) {
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) tma_store<kGw, false>(&tmO, slab, col, row, t.e);
+                        if (lane == 0) tma_store<kGw>(&tmO, slab, col, row, t.e);
                     } else {
                         store_slab<Out>(slab, lane, p.N - col, at_col(static_cast<Out*>(p.out), col));
                         // an empty group, so that the groups count the slabs' uses
