@@ -134,8 +134,21 @@ typedef enum { MOE_DISPATCH_AUTO = 0, MOE_DISPATCH_COPY = 1, MOE_DISPATCH_GATHER
  *                       page §3): the layer uses the weights codes * scale.
  *                       bf16 activations only.  Built for decode-sized batches
  *                       (a few rows per expert): it halves the weight bytes the
- *                       FFNs stream.  Shared experts keep native weights. */
-typedef enum { MOE_WEIGHTS_NATIVE = 0, MOE_WEIGHTS_INT8 = 1 } moe_weight_format_t;
+ *                       FFNs stream.  Shared experts keep native weights.
+ *   MOE_WEIGHTS_INT4_G32, _G64, _G128  4-bit codes with an fp32 scale per
+ *                       expert, output column and group of 32, 64 or 128
+ *                       consecutive K (the value is the group length; from
+ *                       moe_quantize_int4 or moe_pack_int4).  bf16 activations
+ *                       only, shared experts native, as INT8; 0.27 to 0.31 of
+ *                       the bytes of bf16 weights.  Sums in fp32: the codes are
+ *                       multiplied exactly and each group's sum by its scale. */
+typedef enum {
+    MOE_WEIGHTS_NATIVE = 0,
+    MOE_WEIGHTS_INT8 = 1,
+    MOE_WEIGHTS_INT4_G32 = 32,
+    MOE_WEIGHTS_INT4_G64 = 64,
+    MOE_WEIGHTS_INT4_G128 = 128
+} moe_weight_format_t;
 
 /* Where moe_forward and moe_dp_finish apply the routing weights topk_w.
  *   MOE_WEIGHTING_AUTO      the library's choice: EPILOGUE where it applies
@@ -190,7 +203,9 @@ typedef struct {
     const void* shared_down_or_w2;   /* [S, ffn, d] */
     const void* shared_b1;           /* [S, ffn] GELU only, else NULL */
     const void* shared_b2;           /* [S, d]   GELU only, else NULL */
-    /* MOE_WEIGHTS_INT8: w_gate_or_w1 / w_up / w_down_or_w2 hold int8 codes and these their scales */
+    /* MOE_WEIGHTS_INT8: w_gate_or_w1 / w_up / w_down_or_w2 hold int8 codes and these their scales.
+     * MOE_WEIGHTS_INT4_*: codes in the layout of moe_quantize_int4 ([E, ffn, ceil(d/128) * 64 bytes], down:
+     * [E, d, ceil(ffn/128) * 64 bytes]) and scales [E, ceil(d/group), ffn], down: [E, ceil(ffn/group), d] */
     const float* gate_or_w1_scale;   /* [E, ffn] */
     const float* up_scale;           /* [E, ffn] SwiGLU only, else NULL */
     const float* down_or_w2_scale;   /* [E, d] */
@@ -340,6 +355,28 @@ moe_status_t moe_grouped_gemm_grad_x(const moe_grouped_config_t* cfg, const void
 moe_status_t moe_grouped_gemm_grad_w(const moe_grouped_config_t* cfg, const void* x, const void* dy,
                                      const int32_t* offsets, void* dw, void* db, int32_t grad_dtype,
                                      int32_t accumulate, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* The product with 4-bit weights, for batches of few rows per expert:
+ *   y[r,n] = sum over the groups i of scale[e,i,n] * sum_{k in i} x[r,k] q[e,k,n]  (+ bias[e,n])
+ * with codes q in [-8, 7] and groups of `group` = 32, 64 or 128 consecutive k.
+ * bf16 x, y and bias; K and N multiples of 8 (the last group may be shorter).
+ * Storage of the codes: [E, N, ceil(K/128) * 64 bytes], a code q as q + 8 in
+ * four bits.  Each 64-byte block holds 128 k as 16 little-endian words of 32
+ * bits: word 4 t + i holds k = 32 i + 8 t .. + 7 in the order k, k+2, k+4, k+6,
+ * k+1, k+3, k+5, k+7, low bits first; what stands for k >= K is not used.
+ * scale: float32 [E, ceil(K/group), N].
+ *   moe_quantize_int4  from w [E, K, N] (the config's dtype): scale = max over
+ *     the group |w| / 7, q = rint(w / scale) in fp32, ties to even (all-zero
+ *     groups: scale 0, codes 0).
+ *   moe_pack_int4      from codes q [E, K, N] int8 (clamped to [-8, 7]) that come
+ *     with scales of their own.
+ * K <= 2^22.  The config's rows do not matter to these two. */
+moe_status_t moe_quantize_int4(const moe_grouped_config_t* cfg, const void* w, int32_t group, uint8_t* codes,
+                               float* scale, cudaStream_t stream);
+moe_status_t moe_pack_int4(const moe_grouped_config_t* cfg, const int8_t* q, uint8_t* codes, cudaStream_t stream);
+moe_status_t moe_grouped_gemm_int4(const moe_grouped_config_t* cfg, const void* x, const uint8_t* codes,
+                                   const float* scale, int32_t group, const void* bias, const int32_t* offsets, void* y,
+                                   void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /* Gradients of moe_expert_ffn (SwiGLU: W_down(silu(x W_gate) * x W_up); GELU:
  * W2 gelu(x W1 + b1) + b2), layouts as the weights'.  A NULL pointer leaves

@@ -34,6 +34,10 @@ GEMM_KERNELS = {"auto": MOE_GEMM_AUTO, "one_cta": MOE_GEMM_ONE_CTA, "cta_pair": 
 MOE_DISPATCH_AUTO, MOE_DISPATCH_COPY, MOE_DISPATCH_GATHER = 0, 1, 2
 DISPATCH_MODES = {"auto": MOE_DISPATCH_AUTO, "copy": MOE_DISPATCH_COPY, "gather": MOE_DISPATCH_GATHER}
 MOE_WEIGHTING_AUTO, MOE_WEIGHTING_COMBINE, MOE_WEIGHTING_EPILOGUE = 0, 1, 2
+MOE_WEIGHTS_NATIVE, MOE_WEIGHTS_INT8 = 0, 1
+MOE_WEIGHTS_INT4_G32, MOE_WEIGHTS_INT4_G64, MOE_WEIGHTS_INT4_G128 = 32, 64, 128
+WEIGHT_FORMATS = {"native": MOE_WEIGHTS_NATIVE, "int8": MOE_WEIGHTS_INT8, "int4_g32": MOE_WEIGHTS_INT4_G32,
+                  "int4_g64": MOE_WEIGHTS_INT4_G64, "int4_g128": MOE_WEIGHTS_INT4_G128}
 WEIGHTINGS = {"auto": MOE_WEIGHTING_AUTO, "combine": MOE_WEIGHTING_COMBINE, "epilogue": MOE_WEIGHTING_EPILOGUE}
 
 
@@ -119,7 +123,8 @@ EXPORTED_SYMBOLS = ("moe_status_string", "moe_capacity", "moe_max_rows", "moe_wo
                     "moe_ep_workspace_size", "moe_ep_route", "moe_ep_dispatch", "moe_ep_expert_ffn",
                     "moe_ep_combine", "moe_ipc_export", "moe_ipc_open", "moe_ipc_close",
                     "moe_grouped_workspace_size", "moe_grouped_gemm", "moe_grouped_gemm_grad_x",
-                    "moe_grouped_gemm_grad_w", "moe_expert_ffn_backward_workspace_size", "moe_expert_ffn_backward")
+                    "moe_grouped_gemm_grad_w", "moe_quantize_int4", "moe_pack_int4", "moe_grouped_gemm_int4",
+                    "moe_expert_ffn_backward_workspace_size", "moe_expert_ffn_backward")
 
 
 # ---------------------------------------------------------------- config
@@ -138,7 +143,8 @@ class MoEConfig:
     gemm_kernel: str = "auto"    # "auto" | "one_cta" | "cta_pair"
     dispatch: str = "auto"       # "auto" | "copy" | "gather"
     n_shared: int = 0            # shared experts, applied to every token with weight 1
-    weights: str = "native"      # routed experts' weights: "native" (the dtype) or "int8" (codes + scales)
+    weights: str = "native"      # routed experts' weights: "native" (the dtype), "int8" (codes + scales) or
+    #                              "int4_g32" | "int4_g64" | "int4_g128" (4-bit codes, a scale per group of K)
     weighting: str = "auto"      # routing weights applied in: "auto" | "combine" | "epilogue" (second GEMM)
 
     def c(self) -> MoEConfigC:
@@ -147,7 +153,7 @@ class MoEConfig:
                           MOE_ACT_SWIGLU if self.act == "swiglu" else MOE_ACT_GELU_BIAS,
                           float(self.capacity_factor), float(self.aux_alpha), ROUTER_KERNELS[self.router_kernel],
                           GEMM_KERNELS[self.gemm_kernel], DISPATCH_MODES[self.dispatch], int(self.n_shared),
-                          1 if self.weights == "int8" else 0, WEIGHTINGS[self.weighting])
+                          WEIGHT_FORMATS[self.weights], WEIGHTINGS[self.weighting])
 
     @property
     def torch_dtype(self) -> torch.dtype:
@@ -632,11 +638,15 @@ def moe_quantize_int8(cfg: MoEConfig, w: torch.Tensor, stream=None):
 
 
 def quantize_expert_weights(cfg: MoEConfig, weights: dict, stream=None) -> dict:
-    """A copy of `weights` whose routed experts are stored as INT8 codes plus
-    scales (w_gate/w_up/w_down or w1/w2 replaced by codes, with *_scale added)."""
+    """A copy of `weights` whose routed experts are stored as codes plus scales
+    (w_gate/w_up/w_down or w1/w2 replaced by codes, with *_scale added): 4-bit
+    where cfg.weights says so, else INT8."""
     out = dict(weights)
     for name in (("w_gate", "w_up", "w_down") if cfg.act == "swiglu" else ("w1", "w2")):
-        q, s = moe_quantize_int8(cfg, weights[name], stream)
+        if cfg.weights.startswith("int4"):
+            q, s = moe_quantize_int4(weights[name], WEIGHT_FORMATS[cfg.weights], stream)
+        else:
+            q, s = moe_quantize_int8(cfg, weights[name], stream)
         out[name] = q
         out[name + "_scale"] = s
     return out
@@ -783,4 +793,50 @@ def moe_expert_ffn_backward(cfg: MoEConfig, weights: dict, x_perm, offsets, dy_p
             ctypes.c_size_t, _P)
     _call_on(dev, "moe_expert_ffn_backward", f,
              (ctypes.byref(cfg.c()), ctypes.byref(wc), _ptr(x_perm), _ptr(offsets), _ptr(dy_perm), ctypes.byref(gc),
+              ws.ptr, ws.nbytes), stream)
+
+
+# ---------------------------------------------------------------- 4-bit weights
+def _int4_shapes(E: int, K: int, N: int, group: int) -> tuple:
+    return (E, N, -(-K // 128) * 64), (E, -(-K // group), N)
+
+
+def moe_quantize_int4(w: torch.Tensor, group: int, stream=None) -> tuple:
+    """4-bit codes and per-group scales of expert weights w [E, K, N] (bf16 or
+    float32): (uint8 [E, N, ceil(K/128) * 64], float32 [E, ceil(K/group), N])."""
+    E, K, N = w.shape
+    g = GroupedConfig(0, E, K, N, "bf16" if w.dtype == torch.bfloat16 else "f32")
+    _expect("moe_quantize_int4", w.device, (w, (E, K, N), (g.torch_dtype,)))
+    cs, ss = _int4_shapes(E, K, N, max(int(group), 1))
+    codes = torch.empty(cs, dtype=torch.uint8, device=w.device)
+    scale = torch.empty(ss, dtype=torch.float32, device=w.device)
+    f = _fn("moe_quantize_int4", _GCFG, _P, ctypes.c_int32, _P, _P, _P)
+    _call_on(w.device, "moe_quantize_int4", f, (ctypes.byref(g.c()), _ptr(w), int(group), _ptr(codes), _ptr(scale)),
+             stream)
+    return codes, scale
+
+
+def moe_pack_int4(q: torch.Tensor, stream=None) -> torch.Tensor:
+    """The storage form (uint8 [E, N, ceil(K/128) * 64]) of codes q int8
+    [E, K, N] in [-8, 7]."""
+    E, K, N = q.shape
+    g = GroupedConfig(0, E, K, N)
+    _expect("moe_pack_int4", q.device, (q, (E, K, N), (torch.int8,)))
+    codes = torch.empty(_int4_shapes(E, K, N, 128)[0], dtype=torch.uint8, device=q.device)
+    f = _fn("moe_pack_int4", _GCFG, _P, _P, _P)
+    _call_on(q.device, "moe_pack_int4", f, (ctypes.byref(g.c()), _ptr(q), _ptr(codes)), stream)
+    return codes
+
+
+def moe_grouped_gemm_int4(g: GroupedConfig, x, codes, scale, offsets, y, ws: Workspace, group: int, bias=None,
+                          stream=None) -> None:
+    """y[r] = x[r] W[e] (+ bias[e]) with W as 4-bit codes and per-group scales."""
+    dt = (g.torch_dtype,)
+    cs, ss = _int4_shapes(g.E, g.K, g.N, max(int(group), 1))
+    _expect("moe_grouped_gemm_int4", codes.device, (x, (g.rows, g.K), dt), (codes, cs, (torch.uint8,)),
+            (scale, ss, (torch.float32,)), (y, (g.rows, g.N), dt), (bias, (g.E, g.N), dt),
+            (offsets, (g.E + 1,), (torch.int32,)))
+    f = _fn("moe_grouped_gemm_int4", _GCFG, _P, _P, _P, ctypes.c_int32, _P, _P, _P, _P, ctypes.c_size_t, _P)
+    _call_on(codes.device, "moe_grouped_gemm_int4", f,
+             (ctypes.byref(g.c()), _ptr(x), _ptr(codes), _ptr(scale), int(group), _ptr(bias), _ptr(offsets), _ptr(y),
               ws.ptr, ws.nbytes), stream)

@@ -18,7 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 SOURCES = ["moe_api.cu", "router.cu", "router_v2.cu", "router_sm100.cu", "dispatch.cu", "gemm_sm100.cu", "gemm_sm100_pair.cu", "ffn_simt.cu", "combine.cu",
-           "dispatch_noalloc.cu", "pipeline.cu", "ffn_int8.cu", "grouped_gemm.cu", "grouped_f32.cu"]
+           "dispatch_noalloc.cu", "pipeline.cu", "ffn_int8.cu", "grouped_gemm.cu", "grouped_f32.cu",
+           "ffn_int4.cu"]
 HEADERS = ["common.cuh", "internal.h", "scan.cuh", "gemm_common.cuh", "warp_mma.cuh", "grouped.h"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -111,6 +111,11 @@ cudaError_t launch_grouped_gw_bf16(const GroupedArgs& a, cudaStream_t s);
 cudaError_t launch_grouped_fwd_f32(const GroupedArgs& a, cudaStream_t s);
 cudaError_t launch_grouped_gx_f32(const GroupedArgs& a, cudaStream_t s);
 cudaError_t launch_grouped_gw_f32(const GroupedArgs& a, cudaStream_t s);
+// y = x W (+ bias) with W as 4-bit codes (a.w, see ffn_int4.cu) and scales [E, ceil(K/group), N]; bf16.
+cudaError_t launch_grouped_int4(const GroupedArgs& a, const float* scale, int group, cudaStream_t s);
+// Codes and scales of w [E, K, N], or, with `given` [E, K, N] (values -8..7), its storage form alone.
+cudaError_t launch_quantize_int4(const void* w, bool bf16, const int8_t* given, int E, int K, int N, int group,
+                                 uint8_t* codes, float* scale, cudaStream_t s);
 // db[e,n] (+)= sum over the rows of e of dy[r,n]; db in fp32 (a.out_f32) or bf16.
 cudaError_t launch_grouped_colsum(const GroupedArgs& a, bool dy_bf16, cudaStream_t s);
 // Elementwise over all rows in fp32: from g, u and dh to h (over dh), dg (over g), du (over u).

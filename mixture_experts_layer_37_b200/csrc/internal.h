@@ -209,6 +209,9 @@ struct FfnArgs {
     const float* row_w = nullptr;      // [T*k] or null
     // INT8 weights (w1 / w_up / w2 hold codes): per-expert, per-output-column scales
     bool int8 = false;
+    // 4-bit weights with a scale per int4_group of K (0: none); w1 / w_up / w2 hold codes, the scales below
+    // are [E, ceil(K/group), columns]
+    int int4_group = 0;
     const float* w1_scale = nullptr;   // [E, ffn]
     const float* w_up_scale = nullptr; // [E, ffn] or null
     const float* w2_scale = nullptr;   // [E, d]
@@ -220,6 +223,8 @@ cudaError_t launch_ffn_bf16_sm100(const FfnArgs& a, cudaStream_t s);
 cudaError_t launch_ffn_f32(const FfnArgs& a, cudaStream_t s);
 // bf16 activations, INT8 weights (two launches), and the quantiser.
 cudaError_t launch_ffn_int8(const FfnArgs& a, cudaStream_t s);
+// bf16 activations, 4-bit weights (two launches).
+cudaError_t launch_ffn_int4(const FfnArgs& a, cudaStream_t s);
 cudaError_t launch_quantize_int8(const void* w, bool bf16, int64_t E, int64_t K, int64_t N, int8_t* q, float* scale,
                                  cudaStream_t s);
 

@@ -47,6 +47,14 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 size_t elem_size(const moe_config_t* c) { return c->dtype == MOE_DT_BF16 ? 2 : 4; }
 
+// The group length of a 4-bit format, 0 for the others.
+int int4_group(int32_t format) {
+    return format == MOE_WEIGHTS_INT4_G32 || format == MOE_WEIGHTS_INT4_G64 || format == MOE_WEIGHTS_INT4_G128 ? format : 0;
+}
+bool known_weight_format(int32_t format) {
+    return format == MOE_WEIGHTS_NATIVE || format == MOE_WEIGHTS_INT8 || int4_group(format) != 0;
+}
+
 moe_status_t check_config(const moe_config_t* c) {
     if (c == nullptr) return MOE_ERR_INVALID_ARG;
     if (c->T < 0 || c->d <= 0 || c->ffn <= 0 || c->E <= 0 || c->k <= 0) return MOE_ERR_INVALID_ARG;
@@ -56,11 +64,11 @@ moe_status_t check_config(const moe_config_t* c) {
     if (isnan(c->capacity_factor) || isnan(c->aux_alpha) || c->router_kernel < MOE_ROUTER_AUTO ||
         c->router_kernel > MOE_ROUTER_WARP_MMA_STAGED || c->gemm_kernel < MOE_GEMM_AUTO || c->gemm_kernel > MOE_GEMM_CTA_PAIR ||
         c->dispatch < MOE_DISPATCH_AUTO || c->dispatch > MOE_DISPATCH_GATHER || c->n_shared < 0 ||
-        c->weight_format < MOE_WEIGHTS_NATIVE || c->weight_format > MOE_WEIGHTS_INT8 ||
+        !known_weight_format(c->weight_format) ||
         c->weighting < MOE_WEIGHTING_AUTO || c->weighting > MOE_WEIGHTING_EPILOGUE)
         return MOE_ERR_INVALID_ARG;
     if (c->n_shared > kMaxShared) return MOE_ERR_UNSUPPORTED;
-    if (c->weight_format == MOE_WEIGHTS_INT8 && c->dtype != MOE_DT_BF16) return MOE_ERR_UNSUPPORTED;
+    if (c->weight_format != MOE_WEIGHTS_NATIVE && c->dtype != MOE_DT_BF16) return MOE_ERR_UNSUPPORTED;
     if (c->router_kernel == MOE_ROUTER_TCGEN05 &&
         (c->dtype != MOE_DT_BF16 || c->E % 8 != 0 || c->d % 64 != 0))
         return MOE_ERR_UNSUPPORTED;
@@ -227,7 +235,7 @@ moe_status_t check_weights(const moe_config_t* c, const moe_weights_t* w, bool n
             if (w->b1 == nullptr || w->b2 == nullptr || !aligned16(w->b1) || !aligned16(w->b2))
                 return MOE_ERR_INVALID_ARG;
         }
-        if (c->weight_format == MOE_WEIGHTS_INT8 &&
+        if (c->weight_format != MOE_WEIGHTS_NATIVE &&
             (w->gate_or_w1_scale == nullptr || w->down_or_w2_scale == nullptr ||
              (c->act == MOE_ACT_SWIGLU && w->up_scale == nullptr)))
             return MOE_ERR_INVALID_ARG;
@@ -379,15 +387,16 @@ moe_status_t run_ffn(const moe_config_t* c, const moe_weights_t* w, const void* 
     f.row_w = row_w;
     if ((row_w != nullptr || gather_x != nullptr) && src_assign == nullptr) return MOE_ERR_INVALID_ARG;
     if (row_w != nullptr && !weights_in_epilogue(c)) return MOE_ERR_INVALID_ARG;
-    if (c->weight_format == MOE_WEIGHTS_INT8) {
-        // INT8 routed experts: rows always come from the sorted copy
+    if (c->weight_format != MOE_WEIGHTS_NATIVE) {
+        // INT8 and 4-bit routed experts: rows always come from the sorted copy
         if (x_perm == nullptr) return MOE_ERR_INVALID_ARG;
-        f.int8 = true;
+        f.int4_group = int4_group(c->weight_format);
+        f.int8 = f.int4_group == 0;
         f.gather_x = nullptr;
         f.w1_scale = w->gate_or_w1_scale;
         f.w_up_scale = w->up_scale;
         f.w2_scale = w->down_or_w2_scale;
-        return from_cuda(launch_ffn_int8(f, s));
+        return from_cuda(f.int8 ? launch_ffn_int8(f, s) : launch_ffn_int4(f, s));
     }
     return from_cuda(c->dtype == MOE_DT_BF16 ? launch_ffn_bf16_sm100(f, s) : launch_ffn_f32(f, s));
 }
@@ -1049,6 +1058,8 @@ moe_status_t check_grouped_ws(const void* ws, size_t ws_bytes, size_t need) {
 
 bool given(const void* p) { return p != nullptr && aligned16(p); }
 
+constexpr int32_t kMaxInt4K = 1 << 22;  // blocks of 128 K as one grid dimension of the quantiser
+
 GroupedArgs grouped_args(const moe_grouped_config_t* g, const int32_t* offsets, void* ws) {
     GroupedArgs a;
     a.offsets = offsets;
@@ -1163,6 +1174,49 @@ moe_status_t moe_grouped_gemm_grad_w(const moe_grouped_config_t* cfg, const void
     a.out_f32 = grad_dtype == MOE_DT_F32;
     a.accumulate = accumulate != 0;
     return from_cuda(grouped_gw(a, cfg->dtype == MOE_DT_BF16, stream));
+}
+
+static moe_status_t check_int4(const moe_grouped_config_t* g, int32_t group) {
+    const moe_status_t st = check_grouped(g);
+    if (st != MOE_OK) return st;
+    if (int4_group(group) == 0) return MOE_ERR_INVALID_ARG;
+    if (g->K > kMaxInt4K) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+moe_status_t moe_quantize_int4(const moe_grouped_config_t* cfg, const void* w, int32_t group, uint8_t* codes,
+                               float* scale, cudaStream_t stream) {
+    const moe_status_t st = check_int4(cfg, group);
+    if (st != MOE_OK) return st;
+    if (!given(w) || !given(codes) || !given(scale)) return MOE_ERR_INVALID_ARG;
+    return from_cuda(launch_quantize_int4(w, cfg->dtype == MOE_DT_BF16, nullptr, cfg->E, cfg->K, cfg->N, group, codes,
+                                          scale, stream));
+}
+
+moe_status_t moe_pack_int4(const moe_grouped_config_t* cfg, const int8_t* q, uint8_t* codes, cudaStream_t stream) {
+    const moe_status_t st = check_int4(cfg, MOE_WEIGHTS_INT4_G128);
+    if (st != MOE_OK) return st;
+    if (q == nullptr || !given(codes)) return MOE_ERR_INVALID_ARG;
+    return from_cuda(launch_quantize_int4(nullptr, false, q, cfg->E, cfg->K, cfg->N, MOE_WEIGHTS_INT4_G128, codes, nullptr,
+                                          stream));
+}
+
+moe_status_t moe_grouped_gemm_int4(const moe_grouped_config_t* cfg, const void* x, const uint8_t* codes,
+                                   const float* scale, int32_t group, const void* bias, const int32_t* offsets, void* y,
+                                   void* ws, size_t ws_bytes, cudaStream_t stream) {
+    moe_status_t st = check_int4(cfg, group);
+    if (st != MOE_OK) return st;
+    if (cfg->dtype != MOE_DT_BF16) return MOE_ERR_UNSUPPORTED;
+    if (!given(codes) || !given(scale) || offsets == nullptr || !aligned16(bias)) return MOE_ERR_INVALID_ARG;
+    if (cfg->rows > 0 && (!given(x) || !given(y))) return MOE_ERR_INVALID_ARG;
+    if ((st = check_grouped_ws(ws, ws_bytes, kStatusBytes)) != MOE_OK) return st;
+    if (cfg->rows == 0) return MOE_OK;
+    GroupedArgs a = grouped_args(cfg, offsets, ws);
+    a.x = x;
+    a.w = codes;
+    a.bias = bias;
+    a.y = y;
+    return from_cuda(launch_grouped_int4(a, scale, group, stream));
 }
 
 moe_status_t moe_expert_ffn_backward_workspace_size(const moe_config_t* cfg, size_t* bytes) {
