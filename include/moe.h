@@ -370,7 +370,7 @@ moe_status_t moe_grouped_gemm_grad_w(const moe_grouped_config_t* cfg, const void
  *     groups: scale 0, codes 0).
  *   moe_pack_int4      from codes q [E, K, N] int8 (clamped to [-8, 7]) that come
  *     with scales of their own.
- * K <= 2^22.  The config's rows do not matter to these two. */
+ * K <= 2^22, E * N < 2^31.  The config's rows do not matter to these two. */
 moe_status_t moe_quantize_int4(const moe_grouped_config_t* cfg, const void* w, int32_t group, uint8_t* codes,
                                float* scale, cudaStream_t stream);
 moe_status_t moe_pack_int4(const moe_grouped_config_t* cfg, const int8_t* q, uint8_t* codes, cudaStream_t stream);

@@ -53,6 +53,9 @@ enum WaitSite : uint32_t {
     SITE_GROUPED_OFFSETS = 0x501,
     SITE_GROUPED_TAIL = 0x502,
     SITE_GROUPED_OLD = 0x503,
+    SITE_INT4_MMA_WIDENED = 0x511,
+    SITE_INT4_WIDEN_FULL = 0x512,
+    SITE_INT4_WIDEN_FREE = 0x513,
 };
 
 __host__ __device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }

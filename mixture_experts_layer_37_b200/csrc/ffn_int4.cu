@@ -8,265 +8,457 @@
 // Storage of the codes: [E, N, ceil(K/128) * 64 bytes], K-contiguous per output
 // column, a code q stored as q + 8.  A block of 128 codes is 16 words of 32 bits;
 // word 4 t + i holds the eight codes of k = 32 i + 8 t .. + 7 in the order k,
-// k+2, k+4, k+6, k+1, k+3, k+5, k+7 (low bits first).  One 16-byte load then
-// gives lane (g, t) of a warp its operands of the warp-level MMA (m16n8k16, the
-// weights as the 16-row operand, eight tokens as columns) for four steps of 32 k:
-//   - (w >> 4j) & 0x000F000F, or'ed with 0x4300 in both halves, is the bf16 pair
-//     (128 + c[2j], 128 + c[2j+1]), exactly; minus 136, exactly, the codes;
-//   - the same lane's tokens' values for those k are eight neighbours in x: one
-//     16-byte load, no shuffle.
-// The four lanes of a row cover 32 neighbouring k in each step, so a group of
-// 32, 64 or 128 ends with a step and its scale multiplies the fp32 sum of the
-// group: the weights are never rounded to bf16 products with their scale.
+// k+2, k+4, k+6, k+1, k+3, k+5, k+7 (low bits first): (w >> 4j) & 0x000F000F,
+// or'ed with 0x4300 in both halves, is the bf16 pair (128 + c[2j], 128 + c[2j+1]),
+// exactly; minus 136, exactly, two neighbouring codes.
 //
-// Two shapes of a warp's work, chosen on the host from the mean rows per expert:
-// eight tokens by 16 columns, many warps per SM (decode), or 32 tokens by 32
-// columns (a batch), where each widened code is used four times.  Warps of a CTA
-// split K and are joined in a fixed order through shared memory.  Codes are
-// loaded several blocks ahead into registers, past L1 (each is read once).
-// An expert with more rows than a pass holds streams its codes again from L2.
+// Method: the weights are the 128-row operand of the matrix instruction and come
+// from tensor memory: a thread that owns a column n widens its codes in registers
+// and stores them with tcgen05.st, so that the four times larger bf16 form never
+// passes through shared memory (written and read there it would take 4 x 32 KB
+// of its bandwidth where the codes' own 8 KB arrive in the time of 2).  The
+// tokens are the other operand, read by TMA as they lie.  Each group of 32, 64 or
+// 128 k gets a fresh accumulator, and the thread that owns column n multiplies the
+// finished sums by the group's scale in fp32: weights are never rounded to
+// bf16 products with their scale.
+//
+// One persistent CTA per SM, 448 threads, tiles of 128 columns x TN tokens:
+//   warp 0     TMA producer: 256 k of codes [128 rows x 128 bytes] (SwiGLU: of
+//              gate and of up) and of tokens [TN rows x 256 k] per stage, across
+//              tiles without a pause;
+//   warp 1     issues tcgen05.mma (A in TMEM, M=128, N=TN, K=16);
+//   warps 2-9  widen: two groups of four warps take alternate blocks of 128 k
+//              into four TMEM buffers of 64 columns;
+//   warps 10-13 scale and add each group's sums (four TMEM accumulators), and at
+//              the tile's end activation, bias and the store.
+// TN = 16 for batches of few rows per expert, 64 (SwiGLU 32) for more: the host
+// chooses by the mean.  Every wait is bounded in time, as in the other kernels.
 #include <math.h>
 
+#include "gemm_common.cuh"
 #include "grouped.h"
 
 namespace moe {
 namespace {
 
-constexpr int kBlockK = 128;  // codes of a storage block
-constexpr int kWarps = 8;
+using namespace gemm;
+
+constexpr int kBlockK = 128;                  // codes of a storage block
+constexpr int kCols = 128;                    // output columns of a tile
+constexpr int kCodeStage = kCols * 128;       // 16 KB: two blocks of each column
+constexpr int kWidenWarps = 8, kScaleWarps = 4;
+constexpr int kI4Threads = 32 * (2 + kWidenWarps + kScaleWarps);
+constexpr int kABufs = 4, kACols = 64;        // widened blocks in TMEM: 128 k as 64 columns of bf16 pairs
+constexpr int kDBufs = 4;                     // accumulators in TMEM, one group each
 
 enum { I4_PLAIN = 0, I4_SWIGLU = 1, I4_GELU = 2 };
 
 struct Int4Params {
-    const __nv_bfloat16* x = nullptr;     // [rows, K]
-    const uint8_t* q0 = nullptr;          // codes (SwiGLU: gate)
-    const uint8_t* q1 = nullptr;          // SwiGLU: up
-    const float* s0 = nullptr;            // [E, groups, N]
-    const float* s1 = nullptr;
+    const float* s0 = nullptr;            // [E, groups, N] scales (SwiGLU: gate)
+    const float* s1 = nullptr;            // SwiGLU: up
     const __nv_bfloat16* bias = nullptr;  // [E, N] or null
     __nv_bfloat16* out = nullptr;         // [rows, N]
     const int32_t* offsets = nullptr;     // [E+1]
-    int rows = 0, K = 0, N = 0, groups = 0, blocks = 0;
+    int rows = 0, E = 0, N = 0, groups = 0, blocks = 0, n_tiles = 0;
     DevStatus st;
 };
 
-__device__ __forceinline__ uint4 load_stream(const uint8_t* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
+template <int MODE, int TN>
+struct I4Smem {
+    static constexpr int kMats = MODE == I4_SWIGLU ? 2 : 1;
+    static constexpr int kX = TN * 512;  // 256 k of TN tokens: four boxes of 64 k
+    static constexpr int kStage = kMats * kCodeStage + kX;
+    static constexpr int kStages = 200 * 1024 / kStage < 8 ? 200 * 1024 / kStage : 8;
+    static constexpr int kBytes = kStages * kStage + 512 + 1024 /*alignment*/;
+};
 
 // The codes 2j, 2j+1 of a word as a bf16 pair.
 __device__ __forceinline__ uint32_t widen(uint32_t w, int j) {
-    const uint32_t v = ((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u;
+    uint32_t v;  // (shifted & mask) | bits of 128, as one three-input operation
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w >> (4 * j)), "r"(0x000F000Fu), "r"(0x43004300u));
     const __nv_bfloat162 m = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));  // 136
-    __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), m);
-    return *reinterpret_cast<uint32_t*>(&d);
+    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), m);
+    return *reinterpret_cast<const uint32_t*>(&d);
 }
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
+// 16 columns of this warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
-        "%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem desc], kind::f16.
+__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-__device__ __forceinline__ float silu_i4(float x) { return x / (1.0f + __expf(-x)); }
-__device__ __forceinline__ float gelu_i4(float x) { return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f)); }
+struct I4Tile {
+    int e, row0, rows, n0;
+};
+__device__ __forceinline__ I4Tile i4_tile(int tile, const Int4Params& p, const GroupTables* t, int tn, int& i) {
+    while (t->start[i + 1] * p.n_tiles <= tile) ++i;
+    const int local = tile - t->start[i] * p.n_tiles;
+    const int pass = local / p.n_tiles;
+    I4Tile o;
+    o.e = t->expert[i];
+    o.row0 = t->row0[i] + pass * tn;
+    o.rows = min(tn, t->nrows[i] - pass * tn);
+    o.n0 = (local - pass * p.n_tiles) * kCols;
+    return o;
+}
 
-// GS: steps of 32 k per group.  NT: tokens / 8.  MT: 16-column tiles of a warp
-// (SwiGLU: tile 0 of gate, tile 1 of up, the same columns).  KS: warps that
-// split K; the kWarps / KS others stand side by side along N.  DEPTH: blocks of
-// codes in flight per warp.
-template <int MODE, int GS, int NT, int MT, int KS, int DEPTH>
-__global__ void __launch_bounds__(kWarps * 32) int4_kernel(Int4Params p) {
-    constexpr bool TWO = MODE == I4_SWIGLU;
-    constexpr int kMats = TWO ? 2 : 1;
-    constexpr int kColTiles = MT / kMats;                        // distinct 16-column tiles of a warp
-    constexpr int kCtaCols = kWarps / KS * kColTiles * 16;
-    constexpr int kTok = 8 * NT;
-    __shared__ float red[KS][kMats][kTok][kCtaCols + 4];
-    griddep_wait();  // the rows and offsets of the launches before
+// tmQ0, tmQ1: codes as uint8 [E*N, blocks*64], box [128 rows, 128 bytes], 128-byte swizzle; tmX: tokens
+// [rows, K] bf16, box [TN rows, 64 k], 128-byte swizzle.  GS: steps of 32 k per group.
+template <int MODE, int GS, int TN>
+__global__ void __launch_bounds__(kI4Threads, 1)
+    int4_kernel(const __grid_constant__ CUtensorMap tmQ0, const __grid_constant__ CUtensorMap tmQ1,
+                const __grid_constant__ CUtensorMap tmX, Int4Params p) {
+    using S = I4Smem<MODE, TN>;
+    constexpr int kMats = S::kMats, kStages = S::kStages, kGroups = 4 / GS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * S::kStage);
+    uint64_t* empty = full + kStages;
+    uint64_t* aready = empty + kStages;  // [buffer] widened by four warps
+    uint64_t* afree = aready + kABufs;
+    uint64_t* dfull = afree + kABufs;    // [accumulator] a group's products are done
+    uint64_t* dempty = dfull + kDBufs;
+    uint64_t* drain = dempty + kDBufs;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    __shared__ GroupTables tab;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < kABufs; ++b) {
+            mbar_init(&aready[b], 4);
+            mbar_init(&afree[b], 1);
+        }
+        for (int b = 0; b < kDBufs; ++b) {
+            mbar_init(&dfull[b], 1);
+            mbar_init(&dempty[b], kScaleWarps);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        fence_proxy_async_smem();
+        tma_prefetch_desc(&tmQ0);
+        tma_prefetch_desc(&tmX);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    // the prologue above overlaps the launch before; from here on its results are read
+    griddep_wait();
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int g = lane >> 2, t = lane & 3;
-    const int e = blockIdx.y;
-    int row0, nrows;
-    group_rows(p.offsets, p.rows, e, p.st, row0, nrows);
-    if (nrows == 0) return;
-    const int ks = warp % KS, wn = warp / KS;
-    const int n_cta = blockIdx.x * kCtaCols;
-    // this warp's blocks of K
-    const int per = (p.blocks + KS - 1) / KS;
-    const int b0 = min(ks * per, p.blocks), b1 = min(b0 + per, p.blocks);
-    // code rows and scales of this lane: columns g and g + 8 of each tile (past N: the last column, not stored)
-    const uint8_t* code[MT][2];
-    const float* scale[MT][2];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int n = min(n_cta + (wn * kColTiles + m / kMats) * 16 + g + 8 * h, p.N - 1);
-            const bool up = TWO && (m & 1);
-            code[m][h] = (up ? p.q1 : p.q0) + ((int64_t)e * p.N + n) * p.blocks * 64 + t * 16;
-            scale[m][h] = (up ? p.s1 : p.s0) + (int64_t)e * p.groups * p.N + n;
-        }
-    for (int r0 = 0; r0 < nrows; r0 += kTok) {
-        uint4 buf[DEPTH][MT][2];
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d)
-            if (b0 + d < b1)
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) buf[d][m][h] = load_stream(code[m][h] + (int64_t)(b0 + d) * 64);
-        // tokens of this lane as columns of the MMA: r0 + 8 j + g
-        const __nv_bfloat16* xr[NT];
-        bool held[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            held[j] = r0 + 8 * j + g < nrows;
-            xr[j] = p.x + (int64_t)(row0 + (held[j] ? r0 + 8 * j + g : 0)) * p.K + 8 * t;
-        }
-        auto load_x = [&](uint4 (&v)[NT], int k0) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                v[j] = make_uint4(0, 0, 0, 0);
-                if (held[j] && k0 + 8 * t < p.K) v[j] = __ldg(reinterpret_cast<const uint4*>(xr[j] + k0));
-            }
-        };
-        float sum[MT][NT][4];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) sum[m][j][c] = 0.f;
-        uint4 xa[2][NT];
-        if (b0 < b1) load_x(xa[0], b0 * kBlockK);
-        for (int b = b0; b < b1; b += DEPTH) {
-#pragma unroll
-            for (int d = 0; d < DEPTH; ++d) {
-                if (b + d >= b1) break;
-                const int k0 = (b + d) * kBlockK;
-                float part[MT][NT][4];
-                float sc[MT][2];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k = k0 + 32 * i;
-                    // the next step's tokens (past the end: zeros, not loaded)
-                    load_x(xa[(i + 1) & 1], k + 32 < b1 * kBlockK ? k + 32 : p.K);
-                    if (i % GS == 0) {
-                        const int gi = min(k / (32 * GS), p.groups - 1);
-#pragma unroll
-                        for (int m = 0; m < MT; ++m)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) sc[m][h] = __ldg(scale[m][h] + (int64_t)gi * p.N);
-#pragma unroll
-                        for (int m = 0; m < MT; ++m)
-#pragma unroll
-                            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                                for (int c = 0; c < 4; ++c) part[m][j][c] = 0.f;
+    if (warp == 2) build_group_tables<false>(p.offsets, p.rows, p.E, TN, 0, p.st, &tab, lane);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t a_base = tmem_base, d_base = tmem_base + kABufs * kACols;
+    const int total = tab.start[p.E] * p.n_tiles;
+    const int nst = (p.blocks + 1) / 2;  // stages of a tile
+    const uint64_t tmo = p.st.timeout_ns;
+    auto give_up = [&](uint32_t site) {
+        report_timeout(p.st, site);
+        *abort_flag = 1;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------ TMA producer
+            int stage = 0, place = 0;
+            uint32_t phase = 0, issued_mask = 0, issued_par = 0;
+            bool stop = false;
+            for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
+                if (*abort_flag) break;
+                const I4Tile t = i4_tile(tile, p, &tab, TN, place);
+                for (int st = 0; st < nst; ++st) {
+                    if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, tmo)) {
+                        give_up(SITE_GEMM_PRODUCER_EMPTY);
+                        stop = true;
+                        break;
                     }
+                    uint8_t* s = smem + stage * S::kStage;
+                    mbar_arrive_expect_tx(&full[stage], S::kStage);
+                    tma_load_2d(s, &tmQ0, &full[stage], st * 128, t.e * p.N + t.n0);
+                    if (kMats == 2) tma_load_2d(s + kCodeStage, &tmQ1, &full[stage], st * 128, t.e * p.N + t.n0);
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        const uint32_t w0 = word_of(buf[d][m][0], i), w1 = word_of(buf[d][m][1], i);
-                        uint32_t a[2][4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            a[0][j] = widen(w0, j);
-                            a[1][j] = widen(w1, j);
-                        }
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) {
-                            const uint4& xv = xa[i & 1][j];
-                            mma_bf16(part[m][j], a[0][0], a[1][0], a[0][1], a[1][1], xv.x, xv.y);
-                            mma_bf16(part[m][j], a[0][2], a[1][2], a[0][3], a[1][3], xv.z, xv.w);
-                        }
-                    }
-                    if (i % GS == GS - 1) {
-#pragma unroll
-                        for (int m = 0; m < MT; ++m)
-#pragma unroll
-                            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                                for (int c = 0; c < 4; ++c) sum[m][j][c] = fmaf(sc[m][c >> 1], part[m][j][c], sum[m][j][c]);
+                    for (int b = 0; b < 4; ++b)
+                        tma_load_2d(s + kMats * kCodeStage + b * TN * 128, &tmX, &full[stage], st * 256 + 64 * b, t.row0);
+                    issued_mask |= 1u << stage;
+                    issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
                     }
                 }
-                if (b + d + DEPTH < b1)
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) buf[d][m][h] = load_stream(code[m][h] + (int64_t)(b + d + DEPTH) * 64);
             }
+            // the loads land before the MMAs that read them complete: wait for the last release of every stage
+            for (int s = 0; s < kStages; ++s)
+                if ((issued_mask >> s) & 1u)
+                    if (!mbar_wait_bounded(&empty[s], (issued_par >> s) & 1u, tmo)) give_up(SITE_GEMM_PRODUCER_DRAIN);
         }
-        // the K parts of each output, then added in order
-        __syncthreads();  // the last pass's values are read
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ------------------------------------------------ MMA issuer
+            constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(TN >> 3) << 17) | ((128u >> 4) << 24);
+            int stage = 0;
+            uint32_t phase = 0, nblk = 0, ngrp = 0;  // blocks and groups issued
+            bool stop = false;
+            for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
+                if (*abort_flag) break;
+                for (int st = 0; st < nst && !stop; ++st) {
+                    if (!mbar_wait_bounded(&full[stage], phase, tmo)) {
+                        give_up(SITE_GEMM_MMA_FULL);
+                        stop = true;
+                        break;
+                    }
+                    const uint32_t xs = smem_u32(smem + stage * S::kStage + kMats * kCodeStage);
+                    const int nb = min(2, p.blocks - 2 * st);
+                    for (int b = 0; b < nb * kMats && !stop; ++b, ++nblk) {
+                        const uint32_t ab = nblk % kABufs;
+                        if (!mbar_wait_bounded(&aready[ab], (nblk / kABufs) & 1u, tmo)) {
+                            give_up(SITE_INT4_MMA_WIDENED);
+                            stop = true;
+                            break;
+                        }
+                        const int half = b / kMats;  // which of the stage's blocks of 128 k
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+                        for (int g = 0; g < kGroups; ++g, ++ngrp) {
+                            const uint32_t db = ngrp % kDBufs;
+                            if (!mbar_wait_bounded(&dempty[db], ((ngrp / kDBufs) & 1u) ^ 1u, tmo)) {
+                                give_up(SITE_GEMM_MMA_TMEM_EMPTY);
+                                stop = true;
+                                break;
+                            }
+                            tc_fence_after();
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    red[ks][TWO ? m & 1 : 0][8 * j + 2 * t + (c & 1)][(wn * kColTiles + m / kMats) * 16 + g + 8 * (c >> 1)] =
-                        sum[m][j][c];
-        __syncthreads();
-        const int ntok = min(kTok, nrows - r0);
-        // two neighbouring columns per thread (N is even)
-        for (int i = threadIdx.x; i < ntok * (kCtaCols / 2); i += kWarps * 32) {
-            const int tok = i / (kCtaCols / 2), c = i % (kCtaCols / 2) * 2, n = n_cta + c;
-            if (n >= p.N) continue;
-            float v[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float a = 0.f, u = 0.f;
-#pragma unroll
-                for (int z = 0; z < KS; ++z) {
-                    a += red[z][0][tok][c + h];
-                    if (TWO) u += red[z][kMats - 1][tok][c + h];
+                            for (int k = 0; k < 2 * GS; ++k) {
+                                const int kk = g * 2 * GS + k;  // K=16 step of the block
+                                const uint64_t bd = smem_desc_sw128(xs + (half * 2 + kk / 4) * TN * 128 + (kk % 4) * 32, 16, 1024);
+                                tc_mma_f16_ta(d_base + db * TN, a_base + ab * kACols + kk * 8, bd, kIdesc, k != 0 ? 1u : 0u);
+                            }
+                            tc_commit(&dfull[db]);
+                        }
+                        tc_commit(&afree[ab]);
+                    }
+                    if (stop) break;
+                    tc_commit(&empty[stage]);
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
-                if (p.bias != nullptr) a += __bfloat162float(p.bias[(int64_t)e * p.N + n + h]);
-                v[h] = MODE == I4_SWIGLU ? silu_i4(a) * u : MODE == I4_GELU ? gelu_i4(a) : a;
             }
-            *reinterpret_cast<uint32_t*>(p.out + (int64_t)(row0 + r0 + tok) * p.N + n) = pack_bf16x2(v[0], v[1]);
+            // every MMA issued by this thread has completed before TMEM is freed
+            tc_commit(drain);
+            if (!mbar_wait_bounded(drain, 0, tmo)) give_up(SITE_GEMM_DRAIN);
         }
+        __syncwarp();
+    } else if (warp < 2 + kWidenWarps) {
+        // ---------------------------------------------------- widening
+        const int q = warp & 3;                    // TMEM lanes 32q..32q+31: columns n0 + 32q + lane
+        const uint32_t turn = (uint32_t)(warp - 2) >> 2;  // blocks of this parity
+        const int row = 32 * q + lane;
+        int stage = 0;
+        uint32_t phase = 0, nblk = 0;
+        bool stop = false;
+        for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
+            if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
+            for (int st = 0; st < nst && !stop; ++st) {
+                bool ok = mbar_wait_bounded(&full[stage], phase, tmo);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    if (lane == 0) give_up(SITE_INT4_WIDEN_FULL);
+                    stop = true;
+                    break;
+                }
+                const int nb = min(2, p.blocks - 2 * st);
+                for (int b = 0; b < nb * kMats; ++b, ++nblk) {
+                    if ((nblk & 1u) != turn) continue;
+                    const uint8_t* c = smem + stage * S::kStage + (b % kMats) * kCodeStage + row * 128;
+                    const int half = b / kMats;
+                    uint4 w[4];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        w[t] = *reinterpret_cast<const uint4*>(c + (((4 * half + t) ^ (row & 7)) << 4));
+                    const uint32_t ab = nblk % kABufs;
+                    ok = mbar_wait_bounded(&afree[ab], ((nblk / kABufs) & 1u) ^ 1u, tmo);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        if (lane == 0) give_up(SITE_INT4_WIDEN_FREE);
+                        stop = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t dst = a_base + ((uint32_t)(32 * q) << 16) + ab * kACols;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t v[16];
+#pragma unroll
+                        for (int t = 0; t < 4; ++t)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) v[4 * t + j] = widen(word_of(w[t], i), j);
+                        tmem_st_16(dst + 16 * i, v);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&aready[ab]);
+                }
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------- scales, sums and the store
+        const int q = warp & 3;
+        uint32_t ngrp = 0;
+        int place = 0;
+        bool stop = false;
+        for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
+            if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
+            const I4Tile t = i4_tile(tile, p, &tab, TN, place);
+            const int n = t.n0 + 32 * q + lane;
+            const int nc = min(n, p.N - 1);  // past N: some column's scales, not stored
+            const int64_t sbase = (int64_t)t.e * p.groups * p.N + nc;
+            float acc[kMats][TN];
+#pragma unroll
+            for (int m = 0; m < kMats; ++m)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[m][j] = 0.f;
+            // the scales of a block, loaded a block ahead (behind K: the last group's, times a sum of zero)
+            float sc[kMats][kGroups], next[kMats][kGroups];
+            auto load_scales = [&](int b) {
+#pragma unroll
+                for (int m = 0; m < kMats; ++m)
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g)
+                        next[m][g] = __ldg((m ? p.s1 : p.s0) + sbase + (int64_t)min(b * kGroups + g, p.groups - 1) * p.N);
+            };
+            load_scales(0);
+#pragma unroll 1
+            for (int b = 0; b < p.blocks && !stop; ++b) {
+#pragma unroll
+                for (int m = 0; m < kMats; ++m)
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g) sc[m][g] = next[m][g];
+                if (b + 1 < p.blocks) load_scales(b + 1);
+#pragma unroll
+                for (int m = 0; m < kMats; ++m)
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g) {
+                        const uint32_t db = ngrp % kDBufs;
+                        const bool ok = mbar_wait_bounded(&dfull[db], (ngrp / kDBufs) & 1u, tmo);
+                        if (!__all_sync(0xffffffffu, ok)) stop = true;
+                        ++ngrp;
+                        tc_fence_after();
+                        const uint32_t src = d_base + ((uint32_t)(32 * q) << 16) + db * TN;
+#pragma unroll
+                        for (int c = 0; c < TN; c += 16) {
+                            uint32_t v[16];
+                            tmem_ld_16(src + c, v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                acc[m][c + j] = fmaf(sc[m][g], __uint_as_float(v[j]), acc[m][c + j]);
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&dempty[db]);
+                    }
+            }
+            if (stop) {
+                if (lane == 0) give_up(SITE_GEMM_EPI_TMEM_FULL);
+                break;
+            }
+            if (n < p.N) {
+                const float bias = p.bias != nullptr ? __bfloat162float(p.bias[(int64_t)t.e * p.N + n]) : 0.f;
+                __nv_bfloat16* o = p.out + (int64_t)t.row0 * p.N + n;
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    if (j < t.rows) {
+                        float v = acc[0][j] + bias;
+                        if (MODE == I4_SWIGLU) v = silu_f(v) * acc[kMats - 1][j];
+                        if (MODE == I4_GELU) v = gelu_f(v);
+                        o[(int64_t)j * p.N] = __float2bfloat16_rn(v);
+                    }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, 512);
     }
 }
 
-template <int MODE, int GS, int NT, int MT, int KS, int DEPTH>
-cudaError_t launch_shape(const Int4Params& p, int E, cudaStream_t s) {
-    constexpr int kCtaCols = kWarps / KS * (MT / (MODE == I4_SWIGLU ? 2 : 1)) * 16;
-    const dim3 grid((unsigned)((p.N + kCtaCols - 1) / kCtaCols), (unsigned)E);
-    return launch_kernel(int4_kernel<MODE, GS, NT, MT, KS, DEPTH>, grid, dim3(kWarps * 32), 0, s, p);
+struct Int4Operands {
+    const void* x = nullptr;   // [rows, K]
+    const void* q0 = nullptr;  // codes
+    const void* q1 = nullptr;
+    int K = 0;
+};
+
+template <int MODE, int GS, int TN>
+cudaError_t launch_shape(const Int4Operands& o, Int4Params p, cudaStream_t s) {
+    static std::atomic<bool> attr[64];
+    const cudaError_t err = ensure_smem_attr(attr, int4_kernel<MODE, GS, TN>, I4Smem<MODE, TN>::kBytes);
+    if (err != cudaSuccess) return err;
+    CUtensorMap q0, q1, x;
+    bool ok = make_map_u8(&q0, o.q0, (int64_t)p.E * p.N, (int64_t)p.blocks * 64, 128, kCols);
+    ok = ok && make_map_u8(&q1, MODE == I4_SWIGLU ? o.q1 : o.q0, (int64_t)p.E * p.N, (int64_t)p.blocks * 64, 128, kCols);
+    ok = ok && make_map(&x, o.x, (uint64_t)o.K, (uint64_t)p.rows, (uint64_t)o.K * 2, 64, TN);
+    if (!ok) return cudaErrorInvalidValue;
+    p.n_tiles = (p.N + kCols - 1) / kCols;
+    // experts that can hold a row, and the passes of TN rows
+    const int64_t tiles = (min64(p.E, p.rows) + p.rows / TN) * p.n_tiles;
+    return launch_kernel(int4_kernel<MODE, GS, TN>, dim3((unsigned)min64(tiles, sm_count())), dim3(kI4Threads),
+                         I4Smem<MODE, TN>::kBytes, s, q0, q1, x, p);
 }
 
 template <int MODE, int GS>
-cudaError_t launch_group(const Int4Params& p, int E, cudaStream_t s) {
-    if ((int64_t)p.rows <= 6 * (int64_t)E) return launch_shape<MODE, GS, 1, MODE == I4_SWIGLU ? 2 : 1, 4, 4>(p, E, s);
-    return launch_shape<MODE, GS, 4, 2, 2, 2>(p, E, s);
+cudaError_t launch_group(const Int4Operands& o, const Int4Params& p, cudaStream_t s) {
+    if ((int64_t)p.rows <= 12 * (int64_t)p.E) return launch_shape<MODE, GS, 16>(o, p, s);
+    return launch_shape<MODE, GS, MODE == I4_SWIGLU ? 32 : 64>(o, p, s);
 }
 
 template <int MODE>
-cudaError_t launch_int4(const Int4Params& p, int group, int E, cudaStream_t s) {
-    if (group == 32) return launch_group<MODE, 1>(p, E, s);
-    if (group == 64) return launch_group<MODE, 2>(p, E, s);
-    return launch_group<MODE, 4>(p, E, s);
+cudaError_t launch_int4(const Int4Operands& o, const Int4Params& p, int group, cudaStream_t s) {
+    if (group == 32) return launch_group<MODE, 1>(o, p, s);
+    if (group == 64) return launch_group<MODE, 2>(o, p, s);
+    return launch_group<MODE, 4>(o, p, s);
 }
 
-Int4Params int4_params(const int32_t* offsets, int64_t rows, int K, int N, int group, DevStatus st) {
+Int4Params int4_params(const int32_t* offsets, int64_t rows, int E, int K, int N, int group, DevStatus st) {
     Int4Params p;
     p.offsets = offsets;
     p.rows = (int)rows;
-    p.K = K;
+    p.E = E;
     p.N = N;
     p.groups = (K + group - 1) / group;
     p.blocks = (K + kBlockK - 1) / kBlockK;
@@ -342,37 +534,41 @@ cudaError_t launch_quantize_int4(const void* w, bool bf16, const int8_t* given, 
 }
 
 cudaError_t launch_grouped_int4(const GroupedArgs& a, const float* scale, int group, cudaStream_t s) {
-    Int4Params p = int4_params(a.offsets, a.rows, a.K, a.N, group, a.st);
-    p.x = static_cast<const __nv_bfloat16*>(a.x);
-    p.q0 = static_cast<const uint8_t*>(a.w);
+    Int4Params p = int4_params(a.offsets, a.rows, a.E, a.K, a.N, group, a.st);
     p.s0 = scale;
     p.bias = static_cast<const __nv_bfloat16*>(a.bias);
     p.out = static_cast<__nv_bfloat16*>(a.y);
-    return launch_int4<I4_PLAIN>(p, group, a.E, s);
+    Int4Operands o;
+    o.x = a.x;
+    o.q0 = a.w;
+    o.K = a.K;
+    return launch_int4<I4_PLAIN>(o, p, group, s);
 }
 
 cudaError_t launch_ffn_int4(const FfnArgs& a, cudaStream_t s) {
     if (a.rows_cap <= 0) return cudaSuccess;
     const bool swiglu = a.act == 0;
-    Int4Params p = int4_params(a.offsets, a.rows_cap, a.d, a.ffn, a.int4_group, a.st);
-    p.x = static_cast<const __nv_bfloat16*>(a.x_perm);
-    p.q0 = static_cast<const uint8_t*>(a.w1);
-    p.q1 = static_cast<const uint8_t*>(a.w_up);
+    Int4Params p = int4_params(a.offsets, a.rows_cap, a.E, a.d, a.ffn, a.int4_group, a.st);
     p.s0 = a.w1_scale;
     p.s1 = a.w_up_scale;
     p.bias = swiglu ? nullptr : static_cast<const __nv_bfloat16*>(a.b1);
     p.out = static_cast<__nv_bfloat16*>(a.h);
-    cudaError_t err = swiglu ? launch_int4<I4_SWIGLU>(p, a.int4_group, a.E, s)
-                             : launch_int4<I4_GELU>(p, a.int4_group, a.E, s);
+    Int4Operands o;
+    o.x = a.x_perm;
+    o.q0 = a.w1;
+    o.q1 = a.w_up;
+    o.K = a.d;
+    cudaError_t err = swiglu ? launch_int4<I4_SWIGLU>(o, p, a.int4_group, s) : launch_int4<I4_GELU>(o, p, a.int4_group, s);
     if (err != cudaSuccess) return err;
     if (a.between != nullptr && (err = record_mark(a.between, s)) != cudaSuccess) return err;
-    Int4Params r = int4_params(a.offsets, a.rows_cap, a.ffn, a.d, a.int4_group, a.st);
-    r.x = static_cast<const __nv_bfloat16*>(a.h);
-    r.q0 = static_cast<const uint8_t*>(a.w2);
+    Int4Params r = int4_params(a.offsets, a.rows_cap, a.E, a.ffn, a.d, a.int4_group, a.st);
     r.s0 = a.w2_scale;
     r.bias = swiglu ? nullptr : static_cast<const __nv_bfloat16*>(a.b2);
     r.out = static_cast<__nv_bfloat16*>(a.y_perm);
-    return launch_int4<I4_PLAIN>(r, a.int4_group, a.E, s);
+    o.x = a.h;
+    o.q0 = a.w2;
+    o.K = a.ffn;
+    return launch_int4<I4_PLAIN>(o, r, a.int4_group, s);
 }
 
 }  // namespace moe

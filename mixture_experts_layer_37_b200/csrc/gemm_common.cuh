@@ -177,9 +177,10 @@ __device__ __forceinline__ void epilogue_rows(const GemmParams& p, uint32_t tbas
 bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch, uint32_t box_inner,
               uint32_t box_outer);
 // 3-D tensor [outer, mid, inner] of bf16 or fp32 (contiguous), box [1, box_mid, box_inner], 128-byte swizzle,
-// zero fill; and a 2-D fp32 tensor [outer, inner].
+// zero fill; and a 2-D tensor [outer, inner] of bytes or fp32.
 bool make_map_3d(CUtensorMap* m, const void* base, int64_t outer, int64_t mid, int64_t inner, bool f32,
                  uint32_t box_inner, uint32_t box_mid);
+bool make_map_u8(CUtensorMap* m, const void* base, int64_t outer, int64_t inner, uint32_t box_inner, uint32_t box_outer);
 bool make_map_2d_f32(CUtensorMap* m, const void* base, int64_t outer, int64_t inner, uint32_t box_inner,
                      uint32_t box_outer);
 // The same as make_map for any element type, without swizzle (rows land in shared memory as they are in memory).

@@ -373,17 +373,24 @@ bool make_map_3d(CUtensorMap* m, const void* base, int64_t outer, int64_t mid, i
                dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-bool make_map_2d_f32(CUtensorMap* m, const void* base, int64_t outer, int64_t inner, uint32_t box_inner,
-                     uint32_t box_outer) {
+static bool make_map_2d_of(CUtensorMap* m, CUtensorMapDataType type, uint64_t es, const void* base, int64_t outer,
+                           int64_t inner, uint32_t box_inner, uint32_t box_outer) {
     EncodeTiledFn enc = encode_fn();
     if (enc == nullptr) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
-    const cuuint64_t strides[1] = {(cuuint64_t)inner * 4};
+    const cuuint64_t strides[1] = {(cuuint64_t)inner * es};
     const cuuint32_t box[2] = {box_inner, box_outer};
     const cuuint32_t estr[2] = {1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return enc(m, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool make_map_2d_f32(CUtensorMap* m, const void* base, int64_t outer, int64_t inner, uint32_t box_inner,
+                     uint32_t box_outer) {
+    return make_map_2d_of(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, outer, inner, box_inner, box_outer);
+}
+bool make_map_u8(CUtensorMap* m, const void* base, int64_t outer, int64_t inner, uint32_t box_inner, uint32_t box_outer) {
+    return make_map_2d_of(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, outer, inner, box_inner, box_outer);
 }
 bool make_map_plain(CUtensorMap* m, CUtensorMapDataType dtype, const void* base, uint64_t inner, uint64_t outer,
                     uint64_t pitch, uint32_t box_inner, uint32_t box_outer) {

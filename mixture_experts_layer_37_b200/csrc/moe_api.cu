@@ -1180,7 +1180,7 @@ static moe_status_t check_int4(const moe_grouped_config_t* g, int32_t group) {
     const moe_status_t st = check_grouped(g);
     if (st != MOE_OK) return st;
     if (int4_group(group) == 0) return MOE_ERR_INVALID_ARG;
-    if (g->K > kMaxInt4K) return MOE_ERR_UNSUPPORTED;
+    if (g->K > kMaxInt4K || (int64_t)g->E * g->N >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 

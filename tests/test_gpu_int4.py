@@ -85,6 +85,9 @@ SHAPES = [
     ([0, 0], 3, 128, 64),
     ([40, 0, 33, 7, 64], 1, 360, 136),
     ([8, 100], 0, 1032, 520),
+    ([1, 2], 0, 9000, 40),
+    ([70], 0, 2600, 72),
+    ([300, 0, 5], 1, 640, 264),
 ]
 
 
