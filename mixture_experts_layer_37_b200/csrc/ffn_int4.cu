@@ -23,9 +23,9 @@
 // bf16 products with their scale.
 //
 // One persistent CTA per SM, 448 threads, tiles of 128 columns x TN tokens:
-//   warp 0     TMA producer: 256 k of codes [128 rows x 128 bytes] (SwiGLU: of
-//              gate and of up) and of tokens [TN rows x 256 k] per stage, across
-//              tiles without a pause;
+//   warp 0     TMA producer: 256 k of codes [128 rows x 128 bytes] and their
+//              scales (SwiGLU: of gate and of up) and of tokens [TN rows x 256 k]
+//              per stage, across tiles without a pause;
 //   warp 1     issues tcgen05.mma (A in TMEM, M=128, N=TN, K=16);
 //   warps 2-9  widen: two groups of four warps take alternate blocks of 128 k
 //              into four TMEM buffers of 64 columns;
@@ -63,11 +63,13 @@ struct Int4Params {
     DevStatus st;
 };
 
-template <int MODE, int TN>
+template <int MODE, int GS, int TN>
 struct I4Smem {
     static constexpr int kMats = MODE == I4_SWIGLU ? 2 : 1;
     static constexpr int kX = TN * 512;  // 256 k of TN tokens: four boxes of 64 k
-    static constexpr int kStage = kMats * kCodeStage + kX;
+    static constexpr int kScales = 2 * (4 / GS) * kCols * 4;  // the groups of 256 k of 128 columns
+    static constexpr int kXOff = kMats * kCodeStage, kScaleOff = kXOff + kX;
+    static constexpr int kStage = kScaleOff + kMats * kScales;
     static constexpr int kStages = 200 * 1024 / kStage < 8 ? 200 * 1024 / kStage : 8;
     static constexpr int kBytes = kStages * kStage + 512 + 1024 /*alignment*/;
 };
@@ -123,12 +125,14 @@ __device__ __forceinline__ I4Tile i4_tile(int tile, const Int4Params& p, const G
 }
 
 // tmQ0, tmQ1: codes as uint8 [E*N, blocks*64], box [128 rows, 128 bytes], 128-byte swizzle; tmX: tokens
-// [rows, K] bf16, box [TN rows, 64 k], 128-byte swizzle.  GS: steps of 32 k per group.
+// [rows, K] bf16, box [TN rows, 64 k], 128-byte swizzle; tmS0, tmS1: scales [E, groups, N], box [1, the groups
+// of 256 k, 128 columns], zeros past an expert's last group.  GS: steps of 32 k per group.
 template <int MODE, int GS, int TN>
 __global__ void __launch_bounds__(kI4Threads, 1)
     int4_kernel(const __grid_constant__ CUtensorMap tmQ0, const __grid_constant__ CUtensorMap tmQ1,
-                const __grid_constant__ CUtensorMap tmX, Int4Params p) {
-    using S = I4Smem<MODE, TN>;
+                const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmS0,
+                const __grid_constant__ CUtensorMap tmS1, Int4Params p) {
+    using S = I4Smem<MODE, GS, TN>;
     constexpr int kMats = S::kMats, kStages = S::kStages, kGroups = 4 / GS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -147,7 +151,7 @@ __global__ void __launch_bounds__(kI4Threads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], 1 + kScaleWarps);
         }
         for (int b = 0; b < kABufs; ++b) {
             mbar_init(&aready[b], 4);
@@ -186,7 +190,7 @@ __global__ void __launch_bounds__(kI4Threads, 1)
     };
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             // ------------------------------------------------ TMA producer
             int stage = 0, place = 0;
             uint32_t phase = 0, issued_mask = 0, issued_par = 0;
@@ -206,7 +210,9 @@ __global__ void __launch_bounds__(kI4Threads, 1)
                     if (kMats == 2) tma_load_2d(s + kCodeStage, &tmQ1, &full[stage], st * 128, t.e * p.N + t.n0);
 #pragma unroll
                     for (int b = 0; b < 4; ++b)
-                        tma_load_2d(s + kMats * kCodeStage + b * TN * 128, &tmX, &full[stage], st * 256 + 64 * b, t.row0);
+                        tma_load_2d(s + S::kXOff + b * TN * 128, &tmX, &full[stage], st * 256 + 64 * b, t.row0);
+                    tma_load_3d(s + S::kScaleOff, &tmS0, &full[stage], t.n0, st * 2 * kGroups, t.e);
+                    if (kMats == 2) tma_load_3d(s + S::kScaleOff + S::kScales, &tmS1, &full[stage], t.n0, st * 2 * kGroups, t.e);
                     issued_mask |= 1u << stage;
                     issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
                     if (++stage == kStages) {
@@ -222,7 +228,7 @@ __global__ void __launch_bounds__(kI4Threads, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             // ------------------------------------------------ MMA issuer
             constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(TN >> 3) << 17) | ((128u >> 4) << 24);
             int stage = 0;
@@ -236,7 +242,7 @@ __global__ void __launch_bounds__(kI4Threads, 1)
                         stop = true;
                         break;
                     }
-                    const uint32_t xs = smem_u32(smem + stage * S::kStage + kMats * kCodeStage);
+                    const uint32_t xs = smem_u32(smem + stage * S::kStage + S::kXOff);
                     const int nb = min(2, p.blocks - 2 * st);
                     for (int b = 0; b < nb * kMats && !stop; ++b, ++nblk) {
                         const uint32_t ab = nblk % kABufs;
@@ -336,60 +342,54 @@ __global__ void __launch_bounds__(kI4Threads, 1)
     } else {
         // ---------------------------------------------------- scales, sums and the store
         const int q = warp & 3;
-        uint32_t ngrp = 0;
-        int place = 0;
+        uint32_t ngrp = 0, phase = 0;
+        int place = 0, stage = 0;
         bool stop = false;
         for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
             if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
             const I4Tile t = i4_tile(tile, p, &tab, TN, place);
             const int n = t.n0 + 32 * q + lane;
-            const int nc = min(n, p.N - 1);  // past N: some column's scales, not stored
-            const int64_t sbase = (int64_t)t.e * p.groups * p.N + nc;
             float acc[kMats][TN];
 #pragma unroll
             for (int m = 0; m < kMats; ++m)
 #pragma unroll
                 for (int j = 0; j < TN; ++j) acc[m][j] = 0.f;
-            // the scales of a block, loaded a block ahead (behind K: the last group's, times a sum of zero)
-            float sc[kMats][kGroups], next[kMats][kGroups];
-            auto load_scales = [&](int b) {
-#pragma unroll
-                for (int m = 0; m < kMats; ++m)
-#pragma unroll
-                    for (int g = 0; g < kGroups; ++g)
-                        next[m][g] = __ldg((m ? p.s1 : p.s0) + sbase + (int64_t)min(b * kGroups + g, p.groups - 1) * p.N);
-            };
-            load_scales(0);
 #pragma unroll 1
-            for (int b = 0; b < p.blocks && !stop; ++b) {
+            for (int st = 0; st < nst && !stop; ++st) {
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[stage], phase, tmo))) stop = true;
+                const float* scales = reinterpret_cast<const float*>(smem + stage * S::kStage + S::kScaleOff) + 32 * q + lane;
+                const int nb = min(2, p.blocks - 2 * st);
+#pragma unroll 1
+                for (int b = 0; b < nb && !stop; ++b) {
 #pragma unroll
-                for (int m = 0; m < kMats; ++m)
+                    for (int m = 0; m < kMats; ++m)
 #pragma unroll
-                    for (int g = 0; g < kGroups; ++g) sc[m][g] = next[m][g];
-                if (b + 1 < p.blocks) load_scales(b + 1);
+                        for (int g = 0; g < kGroups; ++g) {
+                            const float sc = scales[m * (S::kScales / 4) + (b * kGroups + g) * kCols];
+                            const uint32_t db = ngrp % kDBufs;
+                            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&dfull[db], (ngrp / kDBufs) & 1u, tmo))) stop = true;
+                            ++ngrp;
+                            tc_fence_after();
+                            const uint32_t src = d_base + ((uint32_t)(32 * q) << 16) + db * TN;
 #pragma unroll
-                for (int m = 0; m < kMats; ++m)
+                            for (int c = 0; c < TN; c += 16) {
+                                uint32_t v[16];
+                                tmem_ld_16(src + c, v);
+                                tmem_ld_wait();
 #pragma unroll
-                    for (int g = 0; g < kGroups; ++g) {
-                        const uint32_t db = ngrp % kDBufs;
-                        const bool ok = mbar_wait_bounded(&dfull[db], (ngrp / kDBufs) & 1u, tmo);
-                        if (!__all_sync(0xffffffffu, ok)) stop = true;
-                        ++ngrp;
-                        tc_fence_after();
-                        const uint32_t src = d_base + ((uint32_t)(32 * q) << 16) + db * TN;
-#pragma unroll
-                        for (int c = 0; c < TN; c += 16) {
-                            uint32_t v[16];
-                            tmem_ld_16(src + c, v);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                acc[m][c + j] = fmaf(sc[m][g], __uint_as_float(v[j]), acc[m][c + j]);
+                                for (int j = 0; j < 16; ++j) acc[m][c + j] = fmaf(sc, __uint_as_float(v[j]), acc[m][c + j]);
+                            }
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&dempty[db]);
                         }
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&dempty[db]);
-                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[stage]);
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
             }
             if (stop) {
                 if (lane == 0) give_up(SITE_GEMM_EPI_TMEM_FULL);
@@ -427,18 +427,21 @@ struct Int4Operands {
 template <int MODE, int GS, int TN>
 cudaError_t launch_shape(const Int4Operands& o, Int4Params p, cudaStream_t s) {
     static std::atomic<bool> attr[64];
-    const cudaError_t err = ensure_smem_attr(attr, int4_kernel<MODE, GS, TN>, I4Smem<MODE, TN>::kBytes);
+    const cudaError_t err = ensure_smem_attr(attr, int4_kernel<MODE, GS, TN>, I4Smem<MODE, GS, TN>::kBytes);
     if (err != cudaSuccess) return err;
     CUtensorMap q0, q1, x;
     bool ok = make_map_u8(&q0, o.q0, (int64_t)p.E * p.N, (int64_t)p.blocks * 64, 128, kCols);
     ok = ok && make_map_u8(&q1, MODE == I4_SWIGLU ? o.q1 : o.q0, (int64_t)p.E * p.N, (int64_t)p.blocks * 64, 128, kCols);
     ok = ok && make_map(&x, o.x, (uint64_t)o.K, (uint64_t)p.rows, (uint64_t)o.K * 2, 64, TN);
+    CUtensorMap s0, s1;
+    ok = ok && make_map_3d_f32_plain(&s0, p.s0, p.E, p.groups, p.N, kCols, 2 * (4 / GS));
+    ok = ok && make_map_3d_f32_plain(&s1, MODE == I4_SWIGLU ? p.s1 : p.s0, p.E, p.groups, p.N, kCols, 2 * (4 / GS));
     if (!ok) return cudaErrorInvalidValue;
     p.n_tiles = (p.N + kCols - 1) / kCols;
     // experts that can hold a row, and the passes of TN rows
     const int64_t tiles = (min64(p.E, p.rows) + p.rows / TN) * p.n_tiles;
     return launch_kernel(int4_kernel<MODE, GS, TN>, dim3((unsigned)min64(tiles, sm_count())), dim3(kI4Threads),
-                         I4Smem<MODE, TN>::kBytes, s, q0, q1, x, p);
+                         I4Smem<MODE, GS, TN>::kBytes, s, q0, q1, x, s0, s1, p);
 }
 
 template <int MODE, int GS>

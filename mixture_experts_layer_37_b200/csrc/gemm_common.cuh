@@ -172,6 +172,16 @@ __device__ __forceinline__ void epilogue_rows(const GemmParams& p, uint32_t tbas
     }
 }
 
+// tma_load_2d with three coordinates.
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const void* map, uint64_t* bar, int32_t c0, int32_t c1,
+                                            int32_t c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
 // 2-D bf16 tensor [outer, inner] (inner contiguous, row pitch `pitch` bytes),
 // box [box_outer, box_inner], 128-byte swizzle, zero fill out of bounds.
 bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch, uint32_t box_inner,
@@ -180,6 +190,8 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, 
 // zero fill; and a 2-D tensor [outer, inner] of bytes or fp32.
 bool make_map_3d(CUtensorMap* m, const void* base, int64_t outer, int64_t mid, int64_t inner, bool f32,
                  uint32_t box_inner, uint32_t box_mid);
+bool make_map_3d_f32_plain(CUtensorMap* m, const void* base, int64_t outer, int64_t mid, int64_t inner, uint32_t box_inner,
+                           uint32_t box_mid);  // without swizzle
 bool make_map_u8(CUtensorMap* m, const void* base, int64_t outer, int64_t inner, uint32_t box_inner, uint32_t box_outer);
 bool make_map_2d_f32(CUtensorMap* m, const void* base, int64_t outer, int64_t inner, uint32_t box_inner,
                      uint32_t box_outer);

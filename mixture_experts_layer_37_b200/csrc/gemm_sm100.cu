@@ -360,8 +360,8 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, 
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-bool make_map_3d(CUtensorMap* m, const void* base, int64_t outer, int64_t mid, int64_t inner, bool f32,
-                 uint32_t box_inner, uint32_t box_mid) {
+static bool make_map_3d_of(CUtensorMap* m, bool f32, CUtensorMapSwizzle swizzle, const void* base, int64_t outer,
+                           int64_t mid, int64_t inner, uint32_t box_inner, uint32_t box_mid) {
     EncodeTiledFn enc = encode_fn();
     if (enc == nullptr) return false;
     const cuuint64_t es = f32 ? 4 : 2;
@@ -370,8 +370,16 @@ bool make_map_3d(CUtensorMap* m, const void* base, int64_t outer, int64_t mid, i
     const cuuint32_t box[3] = {box_inner, box_mid, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
-               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool make_map_3d(CUtensorMap* m, const void* base, int64_t outer, int64_t mid, int64_t inner, bool f32,
+                 uint32_t box_inner, uint32_t box_mid) {
+    return make_map_3d_of(m, f32, CU_TENSOR_MAP_SWIZZLE_128B, base, outer, mid, inner, box_inner, box_mid);
+}
+bool make_map_3d_f32_plain(CUtensorMap* m, const void* base, int64_t outer, int64_t mid, int64_t inner, uint32_t box_inner,
+                           uint32_t box_mid) {
+    return make_map_3d_of(m, true, CU_TENSOR_MAP_SWIZZLE_NONE, base, outer, mid, inner, box_inner, box_mid);
 }
 static bool make_map_2d_of(CUtensorMap* m, CUtensorMapDataType type, uint64_t es, const void* base, int64_t outer,
                            int64_t inner, uint32_t box_inner, uint32_t box_outer) {

@@ -110,16 +110,7 @@ constexpr uint32_t make_idesc_majors(int m, int n, bool a_mn, bool b_mn) {
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// tma_load_2d and tma_load_2d_pair with three coordinates.
-__device__ __forceinline__ void tma_load_3d(void* smem_dst, const void* map, uint64_t* bar, int32_t c0, int32_t c1,
-                                            int32_t c2) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
-            smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
-}
-
+// tma_load_2d_pair with three coordinates.
 __device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const void* map, uint32_t bar_cluster_addr, int32_t c0,
                                                  int32_t c1, int32_t c2) {
     asm volatile(
@@ -363,7 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
     };
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             // ------------------------------------------------ TMA producer (both CTAs)
             int stage = 0, place = 0;
             uint32_t phase = 0, issued_mask = 0, issued_par = 0;
@@ -429,7 +420,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
                     if (!mbar_wait_bounded(&empty[s], (issued_par >> s) & 1u, tmo)) give_up(SITE_GEMM_PRODUCER_DRAIN);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             if (rank == 0) {
                 // -------------------------------------------- MMA issuer (leader)
                 // Its loop is kept short: with warp-wide votes and an abort check in every block, 236 of a
