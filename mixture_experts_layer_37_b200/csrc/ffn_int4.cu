@@ -27,12 +27,11 @@
 //              scales (SwiGLU: of gate and of up) and of tokens [TN rows x 256 k]
 //              per stage, across tiles without a pause;
 //   warp 1     issues tcgen05.mma (A in TMEM, M=128, N=TN, K=16);
-//   warps 2-9  widen: two groups of four warps take alternate blocks of 128 k
-//              into four TMEM buffers of 64 columns;
-//   warps 10-13 scale and add each group's sums (four TMEM accumulators), and at
-//              the tile's end activation, bias and the store.
-// TN = 16 for batches of few rows per expert, 64 (SwiGLU 32) for more: the host
-// chooses by the mean.  Every wait is bounded in time, as in the other kernels.
+//   warps 2-9  widen: two groups of four warps take alternate units (I4Smem);
+//   warps 10-13 scale and add each group's sums, and at the tile's end
+//              activation, bias and the store.
+// TN = 16 for batches of few rows per expert, 64 (SwiGLU, or groups of 32: 32)
+// for more: the host chooses by the mean.  Every wait is bounded in time, as in the other kernels.
 #include <math.h>
 
 #include "gemm_common.cuh"
@@ -48,8 +47,6 @@ constexpr int kCols = 128;                    // output columns of a tile
 constexpr int kCodeStage = kCols * 128;       // 16 KB: two blocks of each column
 constexpr int kWidenWarps = 8, kScaleWarps = 4;
 constexpr int kI4Threads = 32 * (2 + kWidenWarps + kScaleWarps);
-constexpr int kABufs = 4, kACols = 64;        // widened blocks in TMEM: 128 k as 64 columns of bf16 pairs
-constexpr int kDBufs = 4;                     // accumulators in TMEM, one group each
 
 enum { I4_PLAIN = 0, I4_SWIGLU = 1, I4_GELU = 2 };
 
@@ -70,6 +67,13 @@ struct I4Smem {
     static constexpr int kScales = 2 * (4 / GS) * kCols * 4;  // the groups of 256 k of 128 columns
     static constexpr int kXOff = kMats * kCodeStage, kScaleOff = kXOff + kX;
     static constexpr int kStage = kScaleOff + kMats * kScales;
+    // What is handed on at a time: kUnit blocks of 128 k of one matrix.  Its widened codes (64 columns a block) and
+    // its groups' accumulators (TN columns each) share one of kBufs buffers in TMEM.  Handing on 256 k halves the
+    // issuer's waits and commits, which bound it at TN = 16.
+    static constexpr int kUnit = TN == 16 ? 2 : 1;
+    static constexpr int kACols = kUnit * 64, kDCols = kUnit * (4 / GS) * TN;
+    static constexpr int kBufs = 4 * (kACols + kDCols) <= 512 ? 4 : 2;
+    static_assert(kBufs * (kACols + kDCols) <= 512, "the buffers fit tensor memory");
     static constexpr int kStages = 200 * 1024 / kStage < 8 ? 200 * 1024 / kStage : 8;
     static constexpr int kBytes = kStages * kStage + 512 + 1024 /*alignment*/;
 };
@@ -133,16 +137,15 @@ __global__ void __launch_bounds__(kI4Threads, 1)
                 const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmS0,
                 const __grid_constant__ CUtensorMap tmS1, Int4Params p) {
     using S = I4Smem<MODE, GS, TN>;
-    constexpr int kMats = S::kMats, kStages = S::kStages, kGroups = 4 / GS;
+    constexpr int kMats = S::kMats, kStages = S::kStages, kGroups = 4 / GS, kUnit = S::kUnit, kBufs = S::kBufs;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * S::kStage);
     uint64_t* empty = full + kStages;
-    uint64_t* aready = empty + kStages;  // [buffer] widened by four warps
-    uint64_t* afree = aready + kABufs;
-    uint64_t* dfull = afree + kABufs;    // [accumulator] a group's products are done
-    uint64_t* dempty = dfull + kDBufs;
-    uint64_t* drain = dempty + kDBufs;
+    uint64_t* ready = empty + kStages;  // [buffer] widened, by four warps
+    uint64_t* done = ready + kBufs;     // its products are done: codes free, sums readable
+    uint64_t* taken = done + kBufs;     // its sums are read
+    uint64_t* drain = taken + kBufs;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     __shared__ GroupTables tab;
@@ -151,15 +154,12 @@ __global__ void __launch_bounds__(kI4Threads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1 + kScaleWarps);
+            mbar_init(&empty[s], kScaleWarps);  // the last readers: they wait for the products
         }
-        for (int b = 0; b < kABufs; ++b) {
-            mbar_init(&aready[b], 4);
-            mbar_init(&afree[b], 1);
-        }
-        for (int b = 0; b < kDBufs; ++b) {
-            mbar_init(&dfull[b], 1);
-            mbar_init(&dempty[b], kScaleWarps);
+        for (int b = 0; b < kBufs; ++b) {
+            mbar_init(&ready[b], 4);
+            mbar_init(&done[b], 1);
+            mbar_init(&taken[b], kScaleWarps);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kI4Threads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const uint32_t a_base = tmem_base, d_base = tmem_base + kABufs * kACols;
+    const uint32_t a_base = tmem_base, d_base = tmem_base + kBufs * S::kACols;
     const int total = tab.start[p.E] * p.n_tiles;
     const int nst = (p.blocks + 1) / 2;  // stages of a tile
     const uint64_t tmo = p.st.timeout_ns;
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kI4Threads, 1)
             // ------------------------------------------------ MMA issuer
             constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(TN >> 3) << 17) | ((128u >> 4) << 24);
             int stage = 0;
-            uint32_t phase = 0, nblk = 0, ngrp = 0;  // blocks and groups issued
+            uint32_t phase = 0, u = 0;  // units issued
             bool stop = false;
             for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
                 if (*abort_flag) break;
@@ -242,37 +242,31 @@ __global__ void __launch_bounds__(kI4Threads, 1)
                         stop = true;
                         break;
                     }
-                    const uint32_t xs = smem_u32(smem + stage * S::kStage + S::kXOff);
                     const int nb = min(2, p.blocks - 2 * st);
-                    for (int b = 0; b < nb * kMats && !stop; ++b, ++nblk) {
-                        const uint32_t ab = nblk % kABufs;
-                        if (!mbar_wait_bounded(&aready[ab], (nblk / kABufs) & 1u, tmo)) {
-                            give_up(SITE_INT4_MMA_WIDENED);
-                            stop = true;
-                            break;
-                        }
-                        const int half = b / kMats;  // which of the stage's blocks of 128 k
+                    const uint64_t xd = smem_desc_sw128(smem_u32(smem + stage * S::kStage + S::kXOff), 16, 1024);
+                    for (int b = 0; b < nb && !stop; b += kUnit)
 #pragma unroll
-                        for (int g = 0; g < kGroups; ++g, ++ngrp) {
-                            const uint32_t db = ngrp % kDBufs;
-                            if (!mbar_wait_bounded(&dempty[db], ((ngrp / kDBufs) & 1u) ^ 1u, tmo)) {
-                                give_up(SITE_GEMM_MMA_TMEM_EMPTY);
+                        for (int m = 0; m < kMats; ++m, ++u) {
+                            const uint32_t buf = u % kBufs, par = (u / kBufs) & 1u;
+                            if (!mbar_wait_bounded(&ready[buf], par, tmo) || !mbar_wait_bounded(&taken[buf], par ^ 1u, tmo)) {
+                                give_up(SITE_INT4_MMA_WIDENED);
                                 stop = true;
                                 break;
                             }
                             tc_fence_after();
+                            const uint32_t a = a_base + buf * S::kACols, d = d_base + buf * S::kDCols;
 #pragma unroll
-                            for (int k = 0; k < 2 * GS; ++k) {
-                                const int kk = g * 2 * GS + k;  // K=16 step of the block
-                                const uint64_t bd = smem_desc_sw128(xs + (half * 2 + kk / 4) * TN * 128 + (kk % 4) * 32, 16, 1024);
-                                tc_mma_f16_ta(d_base + db * TN, a_base + ab * kACols + kk * 8, bd, kIdesc, k != 0 ? 1u : 0u);
+                            for (int h = 0; h < kUnit; ++h) {
+                                if (b + h >= nb) break;
+                                const uint64_t xb = xd + (uint32_t)((b + h) * 2 * TN * 128 >> 4);
+#pragma unroll
+                                for (int kk = 0; kk < 8; ++kk)  // K=16 steps of a block, 2 GS of them in a group
+                                    tc_mma_f16_ta(d + (h * kGroups + kk / (2 * GS)) * TN, a + h * 64 + kk * 8,
+                                                  xb + (uint32_t)(((kk / 4) * TN * 128 + (kk % 4) * 32) >> 4), kIdesc,
+                                                  kk % (2 * GS) != 0 ? 1u : 0u);
                             }
-                            tc_commit(&dfull[db]);
+                            tc_commit(&done[buf]);
                         }
-                        tc_commit(&afree[ab]);
-                    }
-                    if (stop) break;
-                    tc_commit(&empty[stage]);
                     if (++stage == kStages) {
                         stage = 0;
                         phase ^= 1u;
@@ -290,7 +284,7 @@ __global__ void __launch_bounds__(kI4Threads, 1)
         const uint32_t turn = (uint32_t)(warp - 2) >> 2;  // blocks of this parity
         const int row = 32 * q + lane;
         int stage = 0;
-        uint32_t phase = 0, nblk = 0;
+        uint32_t phase = 0, u = 0;
         bool stop = false;
         for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
             if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
@@ -302,37 +296,41 @@ __global__ void __launch_bounds__(kI4Threads, 1)
                     break;
                 }
                 const int nb = min(2, p.blocks - 2 * st);
-                for (int b = 0; b < nb * kMats; ++b, ++nblk) {
-                    if ((nblk & 1u) != turn) continue;
-                    const uint8_t* c = smem + stage * S::kStage + (b % kMats) * kCodeStage + row * 128;
-                    const int half = b / kMats;
-                    uint4 w[4];
+                for (int b = 0; b < nb && !stop; b += kUnit)
+                    for (int m = 0; m < kMats; ++m, ++u) {
+                        if ((u & 1u) != turn) continue;
+                        const uint8_t* c = smem + stage * S::kStage + m * kCodeStage + row * 128;
+                        const uint32_t buf = u % kBufs;
+                        uint4 w[kUnit][4];
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        w[t] = *reinterpret_cast<const uint4*>(c + (((4 * half + t) ^ (row & 7)) << 4));
-                    const uint32_t ab = nblk % kABufs;
-                    ok = mbar_wait_bounded(&afree[ab], ((nblk / kABufs) & 1u) ^ 1u, tmo);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        if (lane == 0) give_up(SITE_INT4_WIDEN_FREE);
-                        stop = true;
-                        break;
+                        for (int h = 0; h < kUnit; ++h)
+#pragma unroll
+                            for (int t = 0; t < 4; ++t)
+                                w[h][t] = *reinterpret_cast<const uint4*>(c + (((4 * (b + h) + t) ^ (row & 7)) << 4));
+                        ok = mbar_wait_bounded(&done[buf], ((u / kBufs) & 1u) ^ 1u, tmo);
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            if (lane == 0) give_up(SITE_INT4_WIDEN_FREE);
+                            stop = true;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t dst = a_base + ((uint32_t)(32 * q) << 16) + buf * S::kACols;
+#pragma unroll
+                        for (int h = 0; h < kUnit; ++h)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t v[16];
+#pragma unroll
+                                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j) v[4 * t + j] = widen(word_of(w[h][t], i), j);
+                                tmem_st_16(dst + 64 * h + 16 * i, v);
+                            }
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ready[buf]);
                     }
-                    tc_fence_after();
-                    const uint32_t dst = a_base + ((uint32_t)(32 * q) << 16) + ab * kACols;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t v[16];
-#pragma unroll
-                        for (int t = 0; t < 4; ++t)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) v[4 * t + j] = widen(word_of(w[t], i), j);
-                        tmem_st_16(dst + 16 * i, v);
-                    }
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&aready[ab]);
-                }
                 if (++stage == kStages) {
                     stage = 0;
                     phase ^= 1u;
@@ -342,7 +340,7 @@ __global__ void __launch_bounds__(kI4Threads, 1)
     } else {
         // ---------------------------------------------------- scales, sums and the store
         const int q = warp & 3;
-        uint32_t ngrp = 0, phase = 0;
+        uint32_t u = 0, phase = 0;
         int place = 0, stage = 0;
         bool stop = false;
         for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
@@ -360,31 +358,35 @@ __global__ void __launch_bounds__(kI4Threads, 1)
                 const float* scales = reinterpret_cast<const float*>(smem + stage * S::kStage + S::kScaleOff) + 32 * q + lane;
                 const int nb = min(2, p.blocks - 2 * st);
 #pragma unroll 1
-                for (int b = 0; b < nb && !stop; ++b) {
+                for (int b = 0; b < nb && !stop; b += kUnit) {
 #pragma unroll
-                    for (int m = 0; m < kMats; ++m)
+                    for (int m = 0; m < kMats; ++m, ++u) {
+                        const uint32_t buf = u % kBufs;
+                        float sc[kUnit * kGroups];
 #pragma unroll
-                        for (int g = 0; g < kGroups; ++g) {
-                            const float sc = scales[m * (S::kScales / 4) + (b * kGroups + g) * kCols];
-                            const uint32_t db = ngrp % kDBufs;
-                            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&dfull[db], (ngrp / kDBufs) & 1u, tmo))) stop = true;
-                            ++ngrp;
-                            tc_fence_after();
-                            const uint32_t src = d_base + ((uint32_t)(32 * q) << 16) + db * TN;
+                        for (int g = 0; g < kUnit * kGroups; ++g)  // past the last block: zeros
+                            sc[g] = scales[m * (S::kScales / 4) + (b * kGroups + g) * kCols];
+                        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&done[buf], (u / kBufs) & 1u, tmo))) stop = true;
+                        tc_fence_after();
+                        const uint32_t src = d_base + ((uint32_t)(32 * q) << 16) + buf * S::kDCols;
+#pragma unroll
+                        for (int g = 0; g < kUnit * kGroups; ++g) {
+                            if (b + g / kGroups >= nb) break;
 #pragma unroll
                             for (int c = 0; c < TN; c += 16) {
                                 uint32_t v[16];
-                                tmem_ld_16(src + c, v);
+                                tmem_ld_16(src + g * TN + c, v);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) acc[m][c + j] = fmaf(sc, __uint_as_float(v[j]), acc[m][c + j]);
+                                for (int j = 0; j < 16; ++j)
+                                    acc[m][c + j] = fmaf(sc[g], __uint_as_float(v[j]), acc[m][c + j]);
                             }
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&dempty[db]);
                         }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&taken[buf]);
+                    }
                 }
-                __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[stage]);
                 if (++stage == kStages) {
                     stage = 0;
@@ -447,7 +449,7 @@ cudaError_t launch_shape(const Int4Operands& o, Int4Params p, cudaStream_t s) {
 template <int MODE, int GS>
 cudaError_t launch_group(const Int4Operands& o, const Int4Params& p, cudaStream_t s) {
     if ((int64_t)p.rows <= 12 * (int64_t)p.E) return launch_shape<MODE, GS, 16>(o, p, s);
-    return launch_shape<MODE, GS, MODE == I4_SWIGLU ? 32 : 64>(o, p, s);
+    return launch_shape<MODE, GS, MODE == I4_SWIGLU || GS == 1 ? 32 : 64>(o, p, s);
 }
 
 template <int MODE>
