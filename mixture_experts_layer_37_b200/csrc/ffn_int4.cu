@@ -22,13 +22,13 @@
 // finished sums by the group's scale in fp32: weights are never rounded to
 // bf16 products with their scale.
 //
-// One persistent CTA per SM, 448 threads, tiles of 128 columns x TN tokens:
+// One persistent CTA per SM, tiles of 128 columns x TN tokens:
 //   warp 0     TMA producer: 256 k of codes [128 rows x 128 bytes] and their
 //              scales (SwiGLU: of gate and of up) and of tokens [TN rows x 256 k]
 //              per stage, across tiles without a pause;
 //   warp 1     issues tcgen05.mma (A in TMEM, M=128, N=TN, K=16);
-//   warps 2-9  widen: two groups of four warps take alternate units (I4Smem);
-//   warps 10-13 scale and add each group's sums, and at the tile's end
+//   then two or three groups of four warps that widen, taking units (I4Smem) in turn;
+//   last four warps that scale and add each group's sums, and at the tile's end
 //              activation, bias and the store.
 // TN = 16 for batches of few rows per expert, 64 (SwiGLU, or groups of 32: 32)
 // for more: the host chooses by the mean.  Every wait is bounded in time, as in the other kernels.
@@ -45,8 +45,7 @@ using namespace gemm;
 constexpr int kBlockK = 128;                  // codes of a storage block
 constexpr int kCols = 128;                    // output columns of a tile
 constexpr int kCodeStage = kCols * 128;       // 16 KB: two blocks of each column
-constexpr int kWidenWarps = 8, kScaleWarps = 4;
-constexpr int kI4Threads = 32 * (2 + kWidenWarps + kScaleWarps);
+constexpr int kScaleWarps = 4;
 
 enum { I4_PLAIN = 0, I4_SWIGLU = 1, I4_GELU = 2 };
 
@@ -67,13 +66,22 @@ struct I4Smem {
     static constexpr int kScales = 2 * (4 / GS) * kCols * 4;  // the groups of 256 k of 128 columns
     static constexpr int kXOff = kMats * kCodeStage, kScaleOff = kXOff + kX;
     static constexpr int kStage = kScaleOff + kMats * kScales;
-    // What is handed on at a time: kUnit blocks of 128 k of one matrix.  Its widened codes (64 columns a block) and
-    // its groups' accumulators (TN columns each) share one of kBufs buffers in TMEM.  Handing on 256 k halves the
-    // issuer's waits and commits, which bound it at TN = 16.
+    // What is handed on at a time: kUnit blocks of 128 k of one matrix, its widened codes (64 columns a block) in one
+    // of kABufs buffers in TMEM and its groups' accumulators (TN columns each) in one of kDBufs.  Handing on 256 k
+    // at TN = 16 halves the issuer's waits and commits, about 450 clocks a unit beside 36 for each MMA.
     static constexpr int kUnit = TN == 16 ? 2 : 1;
     static constexpr int kACols = kUnit * 64, kDCols = kUnit * (4 / GS) * TN;
-    static constexpr int kBufs = 4 * (kACols + kDCols) <= 512 ? 4 : 2;
-    static_assert(kBufs * (kACols + kDCols) <= 512, "the buffers fit tensor memory");
+    static constexpr int kABufs = TN != 16 ? 4 : GS == 1 ? 2 : 3;
+    // No more accumulators than A buffers: a buffer's `done` must not complete again before the warps that wait for
+    // it have seen it, and a unit kABufs later waits for their `taken` only if there are no more of these.
+    static constexpr int kDFit = (512 - kABufs * kACols) / kDCols, kDBufs = kDFit < kABufs ? kDFit : kABufs;
+    static_assert(kDBufs >= 2 && kABufs * kACols + kDBufs * kDCols <= 512, "the buffers fit tensor memory");
+    static constexpr int kGroupsOfWarps = kABufs == 3 ? 3 : 2;  // four widening warps each
+    // A group comes back to a buffer that it filled itself the last time: only then does the parity that it waits
+    // for tell that use from the one before.
+    static_assert(kABufs % kGroupsOfWarps == 0, "each buffer belongs to one group of warps");
+    static constexpr int kWidenWarps = 4 * kGroupsOfWarps;
+    static constexpr int kThreads = 32 * (2 + kWidenWarps + kScaleWarps);
     static constexpr int kStages = 200 * 1024 / kStage < 8 ? 200 * 1024 / kStage : 8;
     static constexpr int kBytes = kStages * kStage + 512 + 1024 /*alignment*/;
 };
@@ -113,6 +121,18 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
+// A place in a ring of N buffers and the parity of its current turn.
+template <int N>
+struct Ring {
+    uint32_t i = 0, par = 0;
+    __device__ __forceinline__ void next() {
+        if (++i == N) {
+            i = 0;
+            par ^= 1u;
+        }
+    }
+};
+
 struct I4Tile {
     int e, row0, rows, n0;
 };
@@ -132,20 +152,21 @@ __device__ __forceinline__ I4Tile i4_tile(int tile, const Int4Params& p, const G
 // [rows, K] bf16, box [TN rows, 64 k], 128-byte swizzle; tmS0, tmS1: scales [E, groups, N], box [1, the groups
 // of 256 k, 128 columns], zeros past an expert's last group.  GS: steps of 32 k per group.
 template <int MODE, int GS, int TN>
-__global__ void __launch_bounds__(kI4Threads, 1)
+__global__ void __launch_bounds__(I4Smem<MODE, GS, TN>::kThreads, 1)
     int4_kernel(const __grid_constant__ CUtensorMap tmQ0, const __grid_constant__ CUtensorMap tmQ1,
                 const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmS0,
                 const __grid_constant__ CUtensorMap tmS1, Int4Params p) {
     using S = I4Smem<MODE, GS, TN>;
-    constexpr int kMats = S::kMats, kStages = S::kStages, kGroups = 4 / GS, kUnit = S::kUnit, kBufs = S::kBufs;
+    constexpr int kMats = S::kMats, kStages = S::kStages, kGroups = 4 / GS, kUnit = S::kUnit;
+    constexpr int kABufs = S::kABufs, kDBufs = S::kDBufs;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * S::kStage);
     uint64_t* empty = full + kStages;
-    uint64_t* ready = empty + kStages;  // [buffer] widened, by four warps
-    uint64_t* done = ready + kBufs;     // its products are done: codes free, sums readable
-    uint64_t* taken = done + kBufs;     // its sums are read
-    uint64_t* drain = taken + kBufs;
+    uint64_t* ready = empty + kStages;  // [A buffer] widened, by four warps
+    uint64_t* done = ready + kABufs;    // [A buffer] its products are done: codes free, sums readable
+    uint64_t* taken = done + kABufs;    // [D buffer] its sums are read
+    uint64_t* drain = taken + kDBufs;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     __shared__ GroupTables tab;
@@ -156,11 +177,11 @@ __global__ void __launch_bounds__(kI4Threads, 1)
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], kScaleWarps);  // the last readers: they wait for the products
         }
-        for (int b = 0; b < kBufs; ++b) {
+        for (int b = 0; b < kABufs; ++b) {
             mbar_init(&ready[b], 4);
             mbar_init(&done[b], 1);
-            mbar_init(&taken[b], kScaleWarps);
         }
+        for (int b = 0; b < kDBufs; ++b) mbar_init(&taken[b], kScaleWarps);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -180,7 +201,7 @@ __global__ void __launch_bounds__(kI4Threads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const uint32_t a_base = tmem_base, d_base = tmem_base + kBufs * S::kACols;
+    const uint32_t a_base = tmem_base, d_base = tmem_base + kABufs * S::kACols;
     const int total = tab.start[p.E] * p.n_tiles;
     const int nst = (p.blocks + 1) / 2;  // stages of a tile
     const uint64_t tmo = p.st.timeout_ns;
@@ -232,7 +253,9 @@ __global__ void __launch_bounds__(kI4Threads, 1)
             // ------------------------------------------------ MMA issuer
             constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(TN >> 3) << 17) | ((128u >> 4) << 24);
             int stage = 0;
-            uint32_t phase = 0, u = 0;  // units issued
+            uint32_t phase = 0;
+            Ring<kABufs> ab;
+            Ring<kDBufs> db;
             bool stop = false;
             for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
                 if (*abort_flag) break;
@@ -246,15 +269,15 @@ __global__ void __launch_bounds__(kI4Threads, 1)
                     const uint64_t xd = smem_desc_sw128(smem_u32(smem + stage * S::kStage + S::kXOff), 16, 1024);
                     for (int b = 0; b < nb && !stop; b += kUnit)
 #pragma unroll
-                        for (int m = 0; m < kMats; ++m, ++u) {
-                            const uint32_t buf = u % kBufs, par = (u / kBufs) & 1u;
-                            if (!mbar_wait_bounded(&ready[buf], par, tmo) || !mbar_wait_bounded(&taken[buf], par ^ 1u, tmo)) {
+                        for (int m = 0; m < kMats; ++m) {
+                            if (!mbar_wait_bounded(&ready[ab.i], ab.par, tmo) ||
+                                !mbar_wait_bounded(&taken[db.i], db.par ^ 1u, tmo)) {
                                 give_up(SITE_INT4_MMA_WIDENED);
                                 stop = true;
                                 break;
                             }
                             tc_fence_after();
-                            const uint32_t a = a_base + buf * S::kACols, d = d_base + buf * S::kDCols;
+                            const uint32_t a = a_base + ab.i * S::kACols, d = d_base + db.i * S::kDCols;
 #pragma unroll
                             for (int h = 0; h < kUnit; ++h) {
                                 if (b + h >= nb) break;
@@ -265,7 +288,9 @@ __global__ void __launch_bounds__(kI4Threads, 1)
                                                   xb + (uint32_t)(((kk / 4) * TN * 128 + (kk % 4) * 32) >> 4), kIdesc,
                                                   kk % (2 * GS) != 0 ? 1u : 0u);
                             }
-                            tc_commit(&done[buf]);
+                            tc_commit(&done[ab.i]);
+                            ab.next();
+                            db.next();
                         }
                     if (++stage == kStages) {
                         stage = 0;
@@ -278,43 +303,45 @@ __global__ void __launch_bounds__(kI4Threads, 1)
             if (!mbar_wait_bounded(drain, 0, tmo)) give_up(SITE_GEMM_DRAIN);
         }
         __syncwarp();
-    } else if (warp < 2 + kWidenWarps) {
+    } else if (warp < 2 + S::kWidenWarps) {
         // ---------------------------------------------------- widening
         const int q = warp & 3;                    // TMEM lanes 32q..32q+31: columns n0 + 32q + lane
-        const uint32_t turn = (uint32_t)(warp - 2) >> 2;  // blocks of this parity
+        int turn = (warp - 2) >> 2;                // units until this group's next
         const int row = 32 * q + lane;
         int stage = 0;
-        uint32_t phase = 0, u = 0;
+        uint32_t phase = 0;
+        Ring<kABufs> ab;
         bool stop = false;
         for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
             if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
             for (int st = 0; st < nst && !stop; ++st) {
-                bool ok = mbar_wait_bounded(&full[stage], phase, tmo);
+                const int nb = min(2, p.blocks - 2 * st);
+                // only a stage with a unit of this group is waited for: it cannot be filled again before that is done
+                bool ok = turn >= (nb + kUnit - 1) / kUnit * kMats || mbar_wait_bounded(&full[stage], phase, tmo);
                 if (!__all_sync(0xffffffffu, ok)) {
                     if (lane == 0) give_up(SITE_INT4_WIDEN_FULL);
                     stop = true;
                     break;
                 }
-                const int nb = min(2, p.blocks - 2 * st);
                 for (int b = 0; b < nb && !stop; b += kUnit)
-                    for (int m = 0; m < kMats; ++m, ++u) {
-                        if ((u & 1u) != turn) continue;
+                    for (int m = 0; m < kMats; ++m, ab.next()) {
+                        if (turn-- != 0) continue;
+                        turn = S::kGroupsOfWarps - 1;
                         const uint8_t* c = smem + stage * S::kStage + m * kCodeStage + row * 128;
-                        const uint32_t buf = u % kBufs;
                         uint4 w[kUnit][4];
 #pragma unroll
                         for (int h = 0; h < kUnit; ++h)
 #pragma unroll
                             for (int t = 0; t < 4; ++t)
                                 w[h][t] = *reinterpret_cast<const uint4*>(c + (((4 * (b + h) + t) ^ (row & 7)) << 4));
-                        ok = mbar_wait_bounded(&done[buf], ((u / kBufs) & 1u) ^ 1u, tmo);
+                        ok = mbar_wait_bounded(&done[ab.i], ab.par ^ 1u, tmo);
                         if (!__all_sync(0xffffffffu, ok)) {
                             if (lane == 0) give_up(SITE_INT4_WIDEN_FREE);
                             stop = true;
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t dst = a_base + ((uint32_t)(32 * q) << 16) + buf * S::kACols;
+                        const uint32_t dst = a_base + ((uint32_t)(32 * q) << 16) + ab.i * S::kACols;
 #pragma unroll
                         for (int h = 0; h < kUnit; ++h)
 #pragma unroll
@@ -329,7 +356,7 @@ __global__ void __launch_bounds__(kI4Threads, 1)
                         tmem_st_wait();
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&ready[buf]);
+                        if (lane == 0) mbar_arrive(&ready[ab.i]);
                     }
                 if (++stage == kStages) {
                     stage = 0;
@@ -340,7 +367,9 @@ __global__ void __launch_bounds__(kI4Threads, 1)
     } else {
         // ---------------------------------------------------- scales, sums and the store
         const int q = warp & 3;
-        uint32_t u = 0, phase = 0;
+        uint32_t phase = 0;
+        Ring<kABufs> ab;
+        Ring<kDBufs> db;
         int place = 0, stage = 0;
         bool stop = false;
         for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
@@ -360,15 +389,14 @@ __global__ void __launch_bounds__(kI4Threads, 1)
 #pragma unroll 1
                 for (int b = 0; b < nb && !stop; b += kUnit) {
 #pragma unroll
-                    for (int m = 0; m < kMats; ++m, ++u) {
-                        const uint32_t buf = u % kBufs;
+                    for (int m = 0; m < kMats; ++m) {
                         float sc[kUnit * kGroups];
 #pragma unroll
                         for (int g = 0; g < kUnit * kGroups; ++g)  // past the last block: zeros
                             sc[g] = scales[m * (S::kScales / 4) + (b * kGroups + g) * kCols];
-                        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&done[buf], (u / kBufs) & 1u, tmo))) stop = true;
+                        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&done[ab.i], ab.par, tmo))) stop = true;
                         tc_fence_after();
-                        const uint32_t src = d_base + ((uint32_t)(32 * q) << 16) + buf * S::kDCols;
+                        const uint32_t src = d_base + ((uint32_t)(32 * q) << 16) + db.i * S::kDCols;
 #pragma unroll
                         for (int g = 0; g < kUnit * kGroups; ++g) {
                             if (b + g / kGroups >= nb) break;
@@ -384,7 +412,9 @@ __global__ void __launch_bounds__(kI4Threads, 1)
                         }
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&taken[buf]);
+                        if (lane == 0) mbar_arrive(&taken[db.i]);
+                        ab.next();
+                        db.next();
                     }
                 }
                 if (lane == 0) mbar_arrive(&empty[stage]);
@@ -442,7 +472,7 @@ cudaError_t launch_shape(const Int4Operands& o, Int4Params p, cudaStream_t s) {
     p.n_tiles = (p.N + kCols - 1) / kCols;
     // experts that can hold a row, and the passes of TN rows
     const int64_t tiles = (min64(p.E, p.rows) + p.rows / TN) * p.n_tiles;
-    return launch_kernel(int4_kernel<MODE, GS, TN>, dim3((unsigned)min64(tiles, sm_count())), dim3(kI4Threads),
+    return launch_kernel(int4_kernel<MODE, GS, TN>, dim3((unsigned)min64(tiles, sm_count())), dim3(I4Smem<MODE, GS, TN>::kThreads),
                          I4Smem<MODE, GS, TN>::kBytes, s, q0, q1, x, s0, s1, p);
 }
 
