@@ -70,6 +70,7 @@ struct I4Smem {
     // of kABufs buffers in TMEM and its groups' accumulators (TN columns each) in one of kDBufs.  Handing on 256 k
     // at TN = 16 halves the issuer's waits and commits, about 450 clocks a unit beside 36 for each MMA.
     static constexpr int kUnit = TN == 16 ? 2 : 1;
+    static constexpr int kPerStage = 2 / kUnit * kMats;  // units of a stage: by half, then by matrix
     static constexpr int kACols = kUnit * 64, kDCols = kUnit * (4 / GS) * TN;
     static constexpr int kABufs = TN != 16 ? 4 : GS == 1 ? 2 : 3;
     // No more accumulators than A buffers: a buffer's `done` must not complete again before the warps that wait for
@@ -203,7 +204,12 @@ __global__ void __launch_bounds__(I4Smem<MODE, GS, TN>::kThreads, 1)
     const uint32_t tmem_base = *tmem_slot;
     const uint32_t a_base = tmem_base, d_base = tmem_base + kABufs * S::kACols;
     const int total = tab.start[p.E] * p.n_tiles;
-    const int nst = (p.blocks + 1) / 2;  // stages of a tile
+    // A tile is nst stages; a block of 128 k behind the last one is worked on like the others (codes, tokens and
+    // scales are zeros there), so that every stage holds the same units and only the producer and the last warps
+    // need to know the tiles.
+    const int nst = (p.blocks + 1) / 2;
+    const int tiles = total > (int)blockIdx.x ? (total - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;  // of this CTA
+    const int stages = tiles * nst;
     const uint64_t tmo = p.st.timeout_ns;
     auto give_up = [&](uint32_t site) {
         report_timeout(p.st, site);
@@ -252,50 +258,35 @@ __global__ void __launch_bounds__(I4Smem<MODE, GS, TN>::kThreads, 1)
         if (elect_one()) {
             // ------------------------------------------------ MMA issuer
             constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(TN >> 3) << 17) | ((128u >> 4) << 24);
-            int stage = 0;
-            uint32_t phase = 0;
+            Ring<kStages> sb;
             Ring<kABufs> ab;
             Ring<kDBufs> db;
             bool stop = false;
-            for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
-                if (*abort_flag) break;
-                for (int st = 0; st < nst && !stop; ++st) {
-                    if (!mbar_wait_bounded(&full[stage], phase, tmo)) {
-                        give_up(SITE_GEMM_MMA_FULL);
+            for (int st = 0; st < stages && !stop; ++st, sb.next()) {
+                if (!mbar_wait_bounded(&full[sb.i], sb.par, tmo)) {
+                    give_up(SITE_GEMM_MMA_FULL);
+                    break;
+                }
+                const uint64_t xd = smem_desc_sw128(smem_u32(smem + sb.i * S::kStage + S::kXOff), 16, 1024);
+#pragma unroll
+                for (int v = 0; v < S::kPerStage; ++v) {
+                    if (!mbar_wait_bounded(&ready[ab.i], ab.par, tmo) || !mbar_wait_bounded(&taken[db.i], db.par ^ 1u, tmo)) {
+                        give_up(SITE_INT4_MMA_WIDENED);
                         stop = true;
                         break;
                     }
-                    const int nb = min(2, p.blocks - 2 * st);
-                    const uint64_t xd = smem_desc_sw128(smem_u32(smem + stage * S::kStage + S::kXOff), 16, 1024);
-                    for (int b = 0; b < nb && !stop; b += kUnit)
+                    tc_fence_after();
+                    const uint32_t a = a_base + ab.i * S::kACols, d = d_base + db.i * S::kDCols;
 #pragma unroll
-                        for (int m = 0; m < kMats; ++m) {
-                            if (!mbar_wait_bounded(&ready[ab.i], ab.par, tmo) ||
-                                !mbar_wait_bounded(&taken[db.i], db.par ^ 1u, tmo)) {
-                                give_up(SITE_INT4_MMA_WIDENED);
-                                stop = true;
-                                break;
-                            }
-                            tc_fence_after();
-                            const uint32_t a = a_base + ab.i * S::kACols, d = d_base + db.i * S::kDCols;
-#pragma unroll
-                            for (int h = 0; h < kUnit; ++h) {
-                                if (b + h >= nb) break;
-                                const uint64_t xb = xd + (uint32_t)((b + h) * 2 * TN * 128 >> 4);
-#pragma unroll
-                                for (int kk = 0; kk < 8; ++kk)  // K=16 steps of a block, 2 GS of them in a group
-                                    tc_mma_f16_ta(d + (h * kGroups + kk / (2 * GS)) * TN, a + h * 64 + kk * 8,
-                                                  xb + (uint32_t)(((kk / 4) * TN * 128 + (kk % 4) * 32) >> 4), kIdesc,
-                                                  kk % (2 * GS) != 0 ? 1u : 0u);
-                            }
-                            tc_commit(&done[ab.i]);
-                            ab.next();
-                            db.next();
-                        }
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1u;
+                    for (int kk = 0; kk < 8 * kUnit; ++kk) {  // K=16 steps, 2 GS of them in a group
+                        const int k = v / kMats * 8 + kk;     // of the stage's 16
+                        tc_mma_f16_ta(d + kk / (2 * GS) * TN, a + kk * 8,
+                                      xd + (uint32_t)((k / 4 * TN * 128 + k % 4 * 32) >> 4), kIdesc,
+                                      kk % (2 * GS) != 0 ? 1u : 0u);
                     }
+                    tc_commit(&done[ab.i]);
+                    ab.next();
+                    db.next();
                 }
             }
             // every MMA issued by this thread has completed before TMEM is freed
@@ -306,71 +297,53 @@ __global__ void __launch_bounds__(I4Smem<MODE, GS, TN>::kThreads, 1)
     } else if (warp < 2 + S::kWidenWarps) {
         // ---------------------------------------------------- widening
         const int q = warp & 3;                    // TMEM lanes 32q..32q+31: columns n0 + 32q + lane
-        int turn = (warp - 2) >> 2;                // units until this group's next
         const int row = 32 * q + lane;
-        int stage = 0;
-        uint32_t phase = 0;
-        Ring<kABufs> ab;
-        bool stop = false;
-        for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
-            if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
-            for (int st = 0; st < nst && !stop; ++st) {
-                const int nb = min(2, p.blocks - 2 * st);
-                // only a stage with a unit of this group is waited for: it cannot be filled again before that is done
-                bool ok = turn >= (nb + kUnit - 1) / kUnit * kMats || mbar_wait_bounded(&full[stage], phase, tmo);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    if (lane == 0) give_up(SITE_INT4_WIDEN_FULL);
-                    stop = true;
-                    break;
-                }
-                for (int b = 0; b < nb && !stop; b += kUnit)
-                    for (int m = 0; m < kMats; ++m, ab.next()) {
-                        if (turn-- != 0) continue;
-                        turn = S::kGroupsOfWarps - 1;
-                        const uint8_t* c = smem + stage * S::kStage + m * kCodeStage + row * 128;
-                        uint4 w[kUnit][4];
-#pragma unroll
-                        for (int h = 0; h < kUnit; ++h)
-#pragma unroll
-                            for (int t = 0; t < 4; ++t)
-                                w[h][t] = *reinterpret_cast<const uint4*>(c + (((4 * (b + h) + t) ^ (row & 7)) << 4));
-                        ok = mbar_wait_bounded(&done[ab.i], ab.par ^ 1u, tmo);
-                        if (!__all_sync(0xffffffffu, ok)) {
-                            if (lane == 0) give_up(SITE_INT4_WIDEN_FREE);
-                            stop = true;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t dst = a_base + ((uint32_t)(32 * q) << 16) + ab.i * S::kACols;
-#pragma unroll
-                        for (int h = 0; h < kUnit; ++h)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                uint32_t v[16];
-#pragma unroll
-                                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j) v[4 * t + j] = widen(word_of(w[h][t], i), j);
-                                tmem_st_16(dst + 64 * h + 16 * i, v);
-                            }
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&ready[ab.i]);
-                    }
-                if (++stage == kStages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
+        const uint32_t lanes = (uint32_t)(32 * q) << 16;
+        for (int u = (warp - 2) >> 2; u < stages * S::kPerStage; u += S::kGroupsOfWarps) {
+            const int st = u / S::kPerStage, v = u % S::kPerStage, ab = u % kABufs;
+            const uint8_t* c = smem + st % kStages * S::kStage + v % kMats * kCodeStage + row * 128;
+            // only the stages of its own units are waited for: they cannot be filled again before those are done
+            bool ok = mbar_wait_bounded(&full[st % kStages], (st / kStages) & 1, tmo);
+            if (!__all_sync(0xffffffffu, ok)) {
+                if (lane == 0) give_up(SITE_INT4_WIDEN_FULL);
+                break;
             }
+            uint4 w[kUnit][4];
+#pragma unroll
+            for (int h = 0; h < kUnit; ++h)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    w[h][t] = *reinterpret_cast<const uint4*>(c + (((4 * (v / kMats + h) + t) ^ (row & 7)) << 4));
+            ok = mbar_wait_bounded(&done[ab], ((u / kABufs) & 1) ^ 1, tmo);
+            if (!__all_sync(0xffffffffu, ok)) {
+                if (lane == 0) give_up(SITE_INT4_WIDEN_FREE);
+                break;
+            }
+            tc_fence_after();
+            const uint32_t dst = a_base + lanes + ab * S::kACols;
+#pragma unroll
+            for (int h = 0; h < kUnit; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t r[16];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) r[4 * t + j] = widen(word_of(w[h][t], i), j);
+                    tmem_st_16(dst + 64 * h + 16 * i, r);
+                }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ready[ab]);
         }
     } else {
         // ---------------------------------------------------- scales, sums and the store
         const int q = warp & 3;
-        uint32_t phase = 0;
+        Ring<kStages> sb;
         Ring<kABufs> ab;
         Ring<kDBufs> db;
-        int place = 0, stage = 0;
+        int place = 0;
         bool stop = false;
         for (int tile = blockIdx.x; tile < total && !stop; tile += gridDim.x) {
             if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
@@ -382,46 +355,36 @@ __global__ void __launch_bounds__(I4Smem<MODE, GS, TN>::kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < TN; ++j) acc[m][j] = 0.f;
 #pragma unroll 1
-            for (int st = 0; st < nst && !stop; ++st) {
-                if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[stage], phase, tmo))) stop = true;
-                const float* scales = reinterpret_cast<const float*>(smem + stage * S::kStage + S::kScaleOff) + 32 * q + lane;
-                const int nb = min(2, p.blocks - 2 * st);
-#pragma unroll 1
-                for (int b = 0; b < nb && !stop; b += kUnit) {
+            for (int st = 0; st < nst && !stop; ++st, sb.next()) {
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[sb.i], sb.par, tmo))) stop = true;
+                const float* scales = reinterpret_cast<const float*>(smem + sb.i * S::kStage + S::kScaleOff) + 32 * q + lane;
 #pragma unroll
-                    for (int m = 0; m < kMats; ++m) {
-                        float sc[kUnit * kGroups];
+                for (int v = 0; v < S::kPerStage; ++v) {
+                    constexpr int kG = kUnit * kGroups;  // groups of a unit
+                    const int m = v % kMats;
+                    float sc[kG];
 #pragma unroll
-                        for (int g = 0; g < kUnit * kGroups; ++g)  // past the last block: zeros
-                            sc[g] = scales[m * (S::kScales / 4) + (b * kGroups + g) * kCols];
-                        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&done[ab.i], ab.par, tmo))) stop = true;
-                        tc_fence_after();
-                        const uint32_t src = d_base + ((uint32_t)(32 * q) << 16) + db.i * S::kDCols;
+                    for (int g = 0; g < kG; ++g) sc[g] = scales[m * (S::kScales / 4) + (v / kMats * kGroups + g) * kCols];
+                    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&done[ab.i], ab.par, tmo))) stop = true;
+                    tc_fence_after();
+                    const uint32_t src = d_base + ((uint32_t)(32 * q) << 16) + db.i * S::kDCols;
 #pragma unroll
-                        for (int g = 0; g < kUnit * kGroups; ++g) {
-                            if (b + g / kGroups >= nb) break;
+                    for (int g = 0; g < kG; ++g)
 #pragma unroll
-                            for (int c = 0; c < TN; c += 16) {
-                                uint32_t v[16];
-                                tmem_ld_16(src + g * TN + c, v);
-                                tmem_ld_wait();
+                        for (int c = 0; c < TN; c += 16) {
+                            uint32_t r[16];
+                            tmem_ld_16(src + g * TN + c, r);
+                            tmem_ld_wait();
 #pragma unroll
-                                for (int j = 0; j < 16; ++j)
-                                    acc[m][c + j] = fmaf(sc[g], __uint_as_float(v[j]), acc[m][c + j]);
-                            }
+                            for (int j = 0; j < 16; ++j) acc[m][c + j] = fmaf(sc[g], __uint_as_float(r[j]), acc[m][c + j]);
                         }
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&taken[db.i]);
-                        ab.next();
-                        db.next();
-                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&taken[db.i]);
+                    ab.next();
+                    db.next();
                 }
-                if (lane == 0) mbar_arrive(&empty[stage]);
-                if (++stage == kStages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
+                if (lane == 0) mbar_arrive(&empty[sb.i]);
             }
             if (stop) {
                 if (lane == 0) give_up(SITE_GEMM_EPI_TMEM_FULL);
