@@ -78,13 +78,13 @@ enum { FORM_FWD = 0, FORM_GX = 1, FORM_GW = 2 };
 enum { EPI_BF16 = 0, EPI_F32 = 1, EPI_SWIGLU_GRAD = 2, EPI_GELU_GRAD = 3 };
 
 // fp32 outputs take twice the stores of a bf16 tile: two staging slabs per warp, one stage less.
-template <int EPI>
+template <int FORM, int EPI>
 struct Smem {
-    static constexpr int kSlabs = EPI == EPI_F32 ? 2 : 1;
-    static constexpr int kStages = EPI == EPI_F32 ? 5 : 6;
+    static constexpr int kSlabs = EPI != EPI_F32 ? 1 : FORM == FORM_GW ? 2 : 2;
+    static constexpr int kStages = EPI != EPI_F32 ? 6 : FORM == FORM_GW ? 5 : 5;
     static constexpr int kSlabOff = kStages * kStageBytes;
     static constexpr int kBarOff = kSlabOff + kEpiWarps * kSlabs * kSlabBytes;
-    static constexpr int kBytes = kBarOff + 384 + 1024 /*alignment*/;
+    static constexpr int kBytes = kBarOff + 512 + 1024 /*alignment*/;
 };
 
 struct GroupedParams {
@@ -287,7 +287,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmA2, const __grid_constant__ CUtensorMap tmB2,
                    const __grid_constant__ CUtensorMap tmO, GroupedParams p) {
-    using S = Smem<EPI>;
+    using S = Smem<FORM, EPI>;
     constexpr int kStages = S::kStages;
     constexpr bool kTwoB = EPI == EPI_SWIGLU_GRAD;  // gate and up halves of each CTA's columns
     constexpr bool kGw = FORM == FORM_GW;
@@ -302,8 +302,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
     uint64_t* drain = tempty + 2;
     uint64_t* tail = drain + 1;  // [stage] GW: this CTA's part of an expert's last, partly filled block
     uint64_t* ready = tail + kStages;  // [stage] GW, leader: both CTAs have cleared such a block
-    uint64_t* olds = ready + kStages;  // [epilogue warp][2] GW, fp32: what is there, in the warp's slabs
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(olds + 2 * kEpiWarps);
+    uint64_t* olds = ready + kStages;  // [epilogue warp][kSlabs] GW, fp32: what is there, in the warp's slabs
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(olds + S::kSlabs * kEpiWarps);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     __shared__ GroupTables tab;
 
@@ -322,7 +322,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
         mbar_init(&tempty[0], 2 * kEpiWarps);
         mbar_init(&tempty[1], 2 * kEpiWarps);
         mbar_init(drain, 1);
-        for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(&olds[i], 1);
+        for (int i = 0; i < S::kSlabs * kEpiWarps; ++i) mbar_init(&olds[i], 1);
         *abort_flag = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
@@ -536,7 +536,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
         const int q = warp & 3;            // TMEM lanes 32q..32q+31 are reachable from this warp
         const int hc = (warp - 2) >> 2;    // which half of the columns it takes
         uint8_t* slabs = smem + S::kSlabOff + (warp - 2) * S::kSlabs * kSlabBytes;
-        uint64_t* old = olds + 2 * (warp - 2);
+        uint64_t* old = olds + S::kSlabs * (warp - 2);
         int acc = 0, place = 0, turn = 0;
         uint32_t acc_phase = 0, old_par = 0;
         // the next accumulator, complete; false: gave up
@@ -594,8 +594,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
                     if (lane == 0) {
                         tma_store_wait_read<0>();
 #pragma unroll
-                        for (int s = 0; s < 2; ++s)
-                            if (col0 + 32 * s < p.N) {
+                        for (int s = 0; s < S::kSlabs; ++s)
+                            if (32 * s < ncols && col0 + 32 * s < p.N) {
                                 mbar_arrive_expect_tx(&old[s], kSlabBytes);
                                 tma_load_3d(slabs + s * kSlabBytes, &tmO, &old[s], col0 + 32 * s, row, t.e);
                             }
@@ -604,7 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
                     bool in = true;
 #pragma unroll
                     for (int c = 0; c < 128; c += 32) {
-                        const int s = c / 32 & 1;
+                        const int s = c / 32 % S::kSlabs;
                         if (c >= ncols || col0 + c >= p.N || !in) break;
                         in = __all_sync(0xffffffffu, mbar_wait_bounded(&old[s], (old_par >> s) & 1u, tmo));
                         old_par ^= 1u << s;
@@ -612,9 +612,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
                         for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(x + c + 4 * j) =
                             *slab_piece(slabs + s * kSlabBytes, lane, j);
                         __syncwarp();
-                        if (lane == 0 && in && c + 64 < ncols && col0 + c + 64 < p.N) {
+                        constexpr int kNext = 32 * S::kSlabs;
+                        if (lane == 0 && in && c + kNext < ncols && col0 + c + kNext < p.N) {
                             mbar_arrive_expect_tx(&old[s], kSlabBytes);
-                            tma_load_3d(slabs + s * kSlabBytes, &tmO, &old[s], col0 + c + 64, row, t.e);
+                            tma_load_3d(slabs + s * kSlabBytes, &tmO, &old[s], col0 + c + kNext, row, t.e);
                         }
                     }
                     if (!in) {
@@ -809,12 +810,12 @@ cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap
     int pairs_cap = dev < 64 ? max_pairs[dev].load(std::memory_order_acquire) : 0;
     if (pairs_cap <= 0) {
         cudaError_t err = cudaFuncSetAttribute(grouped_kernel<FORM, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               Smem<EPI>::kBytes);
+                                               Smem<FORM, EPI>::kBytes);
         if (err != cudaSuccess) return err;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * (unsigned)(sm_count() / 2));
         cfg.blockDim = dim3(kThreadsG);
-        cfg.dynamicSmemBytes = Smem<EPI>::kBytes;
+        cfg.dynamicSmemBytes = Smem<FORM, EPI>::kBytes;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
         attr.val.clusterDim.x = 2;
@@ -830,7 +831,7 @@ cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap
     }
     const int pairs = (int)min64(tiles_upper, (int64_t)pairs_cap);
     if (pairs <= 0) return cudaSuccess;
-    return launch_kernel(grouped_kernel<FORM, EPI>, dim3(2 * pairs), dim3(kThreadsG), Smem<EPI>::kBytes, s, a, b, a2, b2,
+    return launch_kernel(grouped_kernel<FORM, EPI>, dim3(2 * pairs), dim3(kThreadsG), Smem<FORM, EPI>::kBytes, s, a, b, a2, b2,
                          o, p);
 }
 
