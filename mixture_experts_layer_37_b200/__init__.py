@@ -673,12 +673,15 @@ class GroupedConfig:
     N: int
     dtype: str = "bf16"        # "bf16" | "f32"
 
-    def c(self) -> MoEGroupedConfigC:
-        return MoEGroupedConfigC(self.rows, self.E, self.K, self.N, MOE_DT_BF16 if self.dtype == "bf16" else MOE_DT_F32)
+    def __post_init__(self):
+        # what every call needs, made once: a small call's time is mostly the host's
+        object.__setattr__(self, "torch_dtype", torch.bfloat16 if self.dtype == "bf16" else torch.float32)
+        object.__setattr__(self, "_c", MoEGroupedConfigC(self.rows, self.E, self.K, self.N,
+                                                         MOE_DT_BF16 if self.dtype == "bf16" else MOE_DT_F32))
+        object.__setattr__(self, "_ref", ctypes.byref(self._c))
 
-    @property
-    def torch_dtype(self) -> torch.dtype:
-        return torch.bfloat16 if self.dtype == "bf16" else torch.float32
+    def c(self) -> MoEGroupedConfigC:
+        return self._c
 
 
 _GCFG = ctypes.POINTER(MoEGroupedConfigC)
@@ -699,20 +702,27 @@ def _fn(name: str, *argtypes):
 def _expect(where: str, device, *specs) -> None:
     """Each (tensor or None, shape, dtypes): a contiguous tensor on `device`."""
     for t, shape, dtypes in specs:
-        if t is None:
-            continue
-        if tuple(t.shape) != shape or t.dtype not in dtypes or not t.is_contiguous() or t.device != device:
+        if t is not None and (t.shape != shape or t.dtype not in dtypes or t.device != device or not t.is_contiguous()):
             raise MoEError(MOE_ERR_INVALID_ARG, f"{where}: a contiguous tensor {list(shape)} of {dtypes} on {device} "
                                                 f"is wanted, got {list(t.shape)} {t.dtype} on {t.device}")
 
 
 def _call_on(device, name: str, f, args, stream) -> None:
     """f(*args, stream) with `device` current (its current stream where none is given)."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        _check(f(*args, _stream(stream)), name)
+    index = device.index
+    if device.type != "cuda":
+        raise MoEError(MOE_ERR_INVALID_ARG, f"{name}: tensors on a CUDA device are wanted, got {device}")
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if index == torch._C._cuda_getDevice():
+        st = f(*args, stream)
     else:
         with torch.cuda.device(device):
-            _check(f(*args, _stream(stream)), name)
+            st = f(*args, stream)
+    if st != MOE_OK:
+        raise MoEError(st, name)
 
 
 def _dtype_code(dtype: torch.dtype) -> int:
@@ -732,7 +742,7 @@ def moe_grouped_gemm(g: GroupedConfig, x, w, offsets, y, ws: Workspace, bias=Non
     _expect("moe_grouped_gemm", w.device, (x, (g.rows, g.K), dt), (w, (g.E, g.K, g.N), dt), (y, (g.rows, g.N), dt),
             (bias, (g.E, g.N), dt), (offsets, (g.E + 1,), (torch.int32,)))
     f = _fn("moe_grouped_gemm", _GCFG, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P)
-    _call_on(w.device, "moe_grouped_gemm", f, (ctypes.byref(g.c()), _ptr(x), _ptr(w), _ptr(bias), _ptr(offsets),
+    _call_on(w.device, "moe_grouped_gemm", f, (g._ref, _ptr(x), _ptr(w), _ptr(bias), _ptr(offsets),
                                                _ptr(y), ws.ptr, ws.nbytes), stream)
 
 
@@ -742,7 +752,7 @@ def moe_grouped_gemm_grad_x(g: GroupedConfig, dy, w, offsets, dx, ws: Workspace,
     _expect("moe_grouped_gemm_grad_x", w.device, (dy, (g.rows, g.N), dt), (w, (g.E, g.K, g.N), dt),
             (dx, (g.rows, g.K), dt), (offsets, (g.E + 1,), (torch.int32,)))
     f = _fn("moe_grouped_gemm_grad_x", _GCFG, _P, _P, _P, _P, _P, ctypes.c_size_t, _P)
-    _call_on(w.device, "moe_grouped_gemm_grad_x", f, (ctypes.byref(g.c()), _ptr(dy), _ptr(w), _ptr(offsets), _ptr(dx),
+    _call_on(w.device, "moe_grouped_gemm_grad_x", f, (g._ref, _ptr(dy), _ptr(w), _ptr(offsets), _ptr(dx),
                                                       ws.ptr, ws.nbytes), stream)
 
 
@@ -756,7 +766,7 @@ def moe_grouped_gemm_grad_w(g: GroupedConfig, x, dy, offsets, dw, ws: Workspace,
     f = _fn("moe_grouped_gemm_grad_w", _GCFG, _P, _P, _P, _P, _P, ctypes.c_int32, ctypes.c_int32, _P, ctypes.c_size_t,
             _P)
     _call_on(dw.device, "moe_grouped_gemm_grad_w", f,
-             (ctypes.byref(g.c()), _ptr(x), _ptr(dy), _ptr(offsets), _ptr(dw), _ptr(db), _dtype_code(dw.dtype),
+             (g._ref, _ptr(x), _ptr(dy), _ptr(offsets), _ptr(dw), _ptr(db), _dtype_code(dw.dtype),
               1 if accumulate else 0, ws.ptr, ws.nbytes), stream)
 
 
@@ -811,7 +821,7 @@ def moe_quantize_int4(w: torch.Tensor, group: int, stream=None) -> tuple:
     codes = torch.empty(cs, dtype=torch.uint8, device=w.device)
     scale = torch.empty(ss, dtype=torch.float32, device=w.device)
     f = _fn("moe_quantize_int4", _GCFG, _P, ctypes.c_int32, _P, _P, _P)
-    _call_on(w.device, "moe_quantize_int4", f, (ctypes.byref(g.c()), _ptr(w), int(group), _ptr(codes), _ptr(scale)),
+    _call_on(w.device, "moe_quantize_int4", f, (g._ref, _ptr(w), int(group), _ptr(codes), _ptr(scale)),
              stream)
     return codes, scale
 
@@ -824,7 +834,7 @@ def moe_pack_int4(q: torch.Tensor, stream=None) -> torch.Tensor:
     _expect("moe_pack_int4", q.device, (q, (E, K, N), (torch.int8,)))
     codes = torch.empty(_int4_shapes(E, K, N, 128)[0], dtype=torch.uint8, device=q.device)
     f = _fn("moe_pack_int4", _GCFG, _P, _P, _P)
-    _call_on(q.device, "moe_pack_int4", f, (ctypes.byref(g.c()), _ptr(q), _ptr(codes)), stream)
+    _call_on(q.device, "moe_pack_int4", f, (g._ref, _ptr(q), _ptr(codes)), stream)
     return codes
 
 
@@ -838,5 +848,5 @@ def moe_grouped_gemm_int4(g: GroupedConfig, x, codes, scale, offsets, y, ws: Wor
             (offsets, (g.E + 1,), (torch.int32,)))
     f = _fn("moe_grouped_gemm_int4", _GCFG, _P, _P, _P, ctypes.c_int32, _P, _P, _P, _P, ctypes.c_size_t, _P)
     _call_on(codes.device, "moe_grouped_gemm_int4", f,
-             (ctypes.byref(g.c()), _ptr(x), _ptr(codes), _ptr(scale), int(group), _ptr(bias), _ptr(offsets), _ptr(y),
+             (g._ref, _ptr(x), _ptr(codes), _ptr(scale), int(group), _ptr(bias), _ptr(offsets), _ptr(y),
               ws.ptr, ws.nbytes), stream)

@@ -5,7 +5,7 @@
 // grouped_gemm.cu.
 //
 // One CTA per output tile, 256 threads, each TM/16 x TN/16 outputs; operands
-// staged 16 deep through shared memory, the next 16 loaded into registers
+// staged TK deep through shared memory, the next TK loaded into registers
 // while the current ones are used; the FMAs run two at a time (f32x2, each
 // rounded as a scalar fmaf).  Every output is one sum in ascending order of
 // the contraction.  Rows and columns outside the expert are never read.
@@ -16,7 +16,6 @@
 namespace moe {
 namespace {
 
-constexpr int TK = 16;
 constexpr int kF32Threads = 256;
 
 enum { FORM_FWD = 0, FORM_GX = 1, FORM_GW = 2 };
@@ -50,7 +49,7 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // contiguous along the tile (KC = false) or along the contraction (KC = true).
 // base points at tile element 0, contraction element 0; ld is the stride of
 // the other axis; t_n, k_n say how many of each exist from here.
-template <int T, bool KC>
+template <int T, int TK, bool KC>
 struct Piece {
     static constexpr int PER = T * TK / 4 / kF32Threads > 0 ? T * TK / 4 / kF32Threads : 1;
     static constexpr bool kAll = T * TK / 4 >= kF32Threads;
@@ -86,8 +85,8 @@ struct Piece {
 };
 
 // A thread's outputs: rows ty*RM + 64*i.. in groups of at most 4, columns the same.
-template <int FORM, int TM, int TN>
-__global__ void __launch_bounds__(kF32Threads) grouped_f32_kernel(F32Params p) {
+template <int FORM, int TM, int TN, int TK>
+__global__ void __launch_bounds__(kF32Threads, 2) grouped_f32_kernel(F32Params p) {
     constexpr int RM = TM / 16, RN = TN / 16;          // outputs per thread: RM rows, RN columns
     constexpr int GM = RM < 4 ? RM : 4, GN = RN < 4 ? RN : 4;  // contiguous run of each
     __shared__ GroupTables tab;
@@ -127,8 +126,8 @@ __global__ void __launch_bounds__(kF32Threads) grouped_f32_kernel(F32Params p) {
         b = p.B + row0 * p.N + n0;
         ldb = p.N;
     }
-    Piece<TM, FORM != FORM_GW> pa;
-    Piece<TN, FORM == FORM_GX> pb;
+    Piece<TM, TK, FORM != FORM_GW> pa;
+    Piece<TN, TK, FORM == FORM_GX> pb;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     uint64_t acc[RM][RN / 2];
 #pragma unroll
@@ -195,23 +194,29 @@ __global__ void __launch_bounds__(kF32Threads) grouped_f32_kernel(F32Params p) {
     }
 }
 
-// Outputs of a tile at most; the choice between 128 x 128 and 64 x 64 tiles: the large ones where
-// they fill the device.
-template <int FORM, int TM, int TN>
+template <int FORM, int TM, int TN, int TK>
 cudaError_t launch_tiles(F32Params p, int out_m, int out_n, cudaStream_t s) {
     p.n_tiles = (out_n + TN - 1) / TN;
     p.m_tiles = (out_m + TM - 1) / TM;
     const int64_t row_tiles = FORM == FORM_GW ? (int64_t)p.E * p.m_tiles : (int64_t)p.rows / TM + p.E;
-    return launch_kernel(grouped_f32_kernel<FORM, TM, TN>, dim3((unsigned)(row_tiles * p.n_tiles)), dim3(kF32Threads),
-                         0, s, p);
+    return launch_kernel(grouped_f32_kernel<FORM, TM, TN, TK>, dim3((unsigned)(row_tiles * p.n_tiles)),
+                         dim3(kF32Threads), 0, s, p);
 }
 
 template <int FORM>
 cudaError_t launch_form(const GroupedArgs& a, const F32Params& p, int out_m, int out_n, cudaStream_t s) {
-    const int64_t big = (FORM == FORM_GW ? (int64_t)a.E * ((out_m + 127) / 128) : (a.rows + 127) / 128) *
-                        ((out_n + 127) / 128);
-    return big >= sm_count() ? launch_tiles<FORM, 128, 128>(p, out_m, out_n, s)
-                             : launch_tiles<FORM, 64, 64>(p, out_m, out_n, s);
+    auto tiles = [&](int tm, int tn) {
+        return (FORM == FORM_GW ? (int64_t)a.E * ((out_m + tm - 1) / tm) : (a.rows + tm - 1) / tm) * ((out_n + tn - 1) / tn);
+    };
+    const int64_t sms = sm_count();
+    // The largest tile that still gives every SM work: 1024 x 1024 weights, 8 experts, 2048 rows, FWD 119 us with
+    // 64 x 128 (256 tiles), 146 us with 64 x 64, 200 us with 128 x 128 (128); GW 101 us with 128 x 128 (512 tiles),
+    // 107 us with 64 x 128; 512 x 512, 512 rows, FWD 24 us with 64 x 64 (64 tiles), 35 us with 64 x 128, 30 us with
+    // 32 x 32; 128 x 256, 4 experts, 128 rows, 4.9 us with 32 x 32, 7.4 us with 64 x 64 (8 tiles).
+    if (FORM == FORM_GW && tiles(128, 128) >= 2 * sms) return launch_tiles<FORM, 128, 128, 16>(p, out_m, out_n, s);
+    if (tiles(64, 128) >= sms) return launch_tiles<FORM, 64, 128, 16>(p, out_m, out_n, s);
+    if (tiles(64, 64) >= sms / 3) return launch_tiles<FORM, 64, 64, 32>(p, out_m, out_n, s);
+    return launch_tiles<FORM, 32, 32, 32>(p, out_m, out_n, s);
 }
 
 F32Params params(const GroupedArgs& a) {
