@@ -27,16 +27,27 @@ __device__ __forceinline__ void group_rows(const int32_t* offsets, int rows, int
     n = ok ? b - a : 0;
 }
 
+// The part z of S of expert e's rows (whole blocks of 64, the last parts may be empty).
+__device__ __forceinline__ void part_rows(int S, int z, int& row0, int& n) {
+    const int per = ((n + S - 1) / S + 63) / 64 * 64, from = min(z * per, n);
+    row0 += from;
+    n = min(per, n - from);
+}
+
 // One warp; each lane holds experts `lane` and `lane + 32`.  BY_ROWS: experts
 // in order of falling row count (ties: lower id) with m_tiles tiles each; else
-// in their own order with one tile per bm rows.
+// in their own order with one tile per bm rows.  split > 1: E counts the parts
+// of the experts' rows, part e % split of expert e / split.
 template <bool BY_ROWS>
 __device__ __forceinline__ void build_group_tables(const int32_t* offsets, int rows, int E, int bm, int m_tiles,
-                                                   const DevStatus& st, GroupTables* t, int lane) {
+                                                   const DevStatus& st, GroupTables* t, int lane, int split = 1) {
     int o[2] = {0, 0}, n[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        if (lane + 32 * i < E) group_rows(offsets, rows, lane + 32 * i, st, o[i], n[i]);
+        if (lane + 32 * i < E) {
+            group_rows(offsets, rows, (lane + 32 * i) / split, st, o[i], n[i]);
+            if (split > 1) part_rows(split, (lane + 32 * i) % split, o[i], n[i]);
+        }
     int rank[2] = {lane, lane + 32};
     if (BY_ROWS) {
         rank[0] = rank[1] = 0;
@@ -93,6 +104,9 @@ struct GroupedArgs {
     void* db = nullptr;                // [E, N] or null
     bool out_f32 = false;              // GX, GW: fp32 output
     bool accumulate = false;           // GW: dw += , db +=
+    // GW, bias gradients: each expert's rows in `split` parts whose sums are written one after the other
+    // ([E, split, ..], fp32, not accumulated) and joined by launch_join
+    int split = 1;
     // GX with a second pair: dx = dy w^T + dy2 w2^T
     const void* dy2 = nullptr;
     const void* w2 = nullptr;          // also: the up matrix of GRAD_SWIGLU
@@ -116,6 +130,9 @@ cudaError_t launch_grouped_int4(const GroupedArgs& a, const float* scale, int gr
 // Codes and scales of w [E, K, N], or, with `given` [E, K, N] (values -8..7), its storage form alone.
 cudaError_t launch_quantize_int4(const void* w, bool bf16, const int8_t* given, int E, int K, int N, int group,
                                  uint8_t* codes, float* scale, cudaStream_t s);
+// out[e, i] (+)= sum over z of part[e, z, i] in ascending z, i < n; out in fp32 or bf16.
+cudaError_t launch_join(const float* part, void* out, bool out_f32, bool accumulate, int E, int split, int64_t n,
+                        cudaStream_t s);
 // db[e,n] (+)= sum over the rows of e of dy[r,n]; db in fp32 (a.out_f32) or bf16.
 cudaError_t launch_grouped_colsum(const GroupedArgs& a, bool dy_bf16, cudaStream_t s);
 // Elementwise over all rows in fp32: from g, u and dh to h (over dh), dg (over g), du (over u).

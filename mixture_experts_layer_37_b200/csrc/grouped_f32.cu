@@ -28,6 +28,7 @@ struct F32Params {
     const int32_t* offsets = nullptr;
     int rows = 0, E = 0, K = 0, N = 0, n_tiles = 0, m_tiles = 0;
     int accumulate = 0;
+    int split = 1;              // GW: parts of each expert's rows; E counts them
     DevStatus st;
 };
 
@@ -95,7 +96,8 @@ __global__ void __launch_bounds__(kF32Threads, 2) grouped_f32_kernel(F32Params p
     griddep_wait();
     griddep_launch_dependents();
     if (threadIdx.x < 32)
-        build_group_tables<FORM == FORM_GW>(p.offsets, p.rows, p.E, TM, p.m_tiles, p.st, &tab, threadIdx.x);
+        build_group_tables<FORM == FORM_GW>(p.offsets, p.rows, p.E, TM, p.m_tiles, p.st, &tab, threadIdx.x,
+                                            FORM == FORM_GW ? p.split : 1);
     __syncthreads();
     const int tile = blockIdx.x;
     if (tile >= tab.start[p.E] * p.n_tiles) return;
@@ -206,7 +208,7 @@ cudaError_t launch_tiles(F32Params p, int out_m, int out_n, cudaStream_t s) {
 template <int FORM>
 cudaError_t launch_form(const GroupedArgs& a, const F32Params& p, int out_m, int out_n, cudaStream_t s) {
     auto tiles = [&](int tm, int tn) {
-        return (FORM == FORM_GW ? (int64_t)a.E * ((out_m + tm - 1) / tm) : (a.rows + tm - 1) / tm) * ((out_n + tn - 1) / tn);
+        return (FORM == FORM_GW ? (int64_t)p.E * ((out_m + tm - 1) / tm) : (a.rows + tm - 1) / tm) * ((out_n + tn - 1) / tn);
     };
     const int64_t sms = sm_count();
     // The largest tile that still gives every SM work: 1024 x 1024 weights, 8 experts, 2048 rows, FWD 119 us with
@@ -238,7 +240,7 @@ struct ColsumParams {
     const void* dy = nullptr;
     void* db = nullptr;
     const int32_t* offsets = nullptr;
-    int rows = 0, N = 0, accumulate = 0;
+    int rows = 0, N = 0, accumulate = 0, split = 1;
     DevStatus st;
 };
 
@@ -251,9 +253,10 @@ __device__ __forceinline__ float4 load4(const void* base, int64_t i) {
     return *reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
 }
 
-// One CTA per (expert, 128 columns): warp w adds the rows w, w+8, ... of its
-// expert in two interleaved sums, and the sixteen sums of a column are added
-// in a fixed order.
+// One CTA per (expert or part of its rows, 128 columns): warp w adds the rows w,
+// w+8, ... in two interleaved sums, eight rows loaded at a time (the loads'
+// latency bounds this kernel), and the sixteen sums of a column are added in a
+// fixed order.
 template <bool IN_BF16, bool OUT_BF16>
 __global__ void __launch_bounds__(kColThreads) colsum_kernel(ColsumParams p) {
     __shared__ float4 part[8][32];
@@ -262,22 +265,25 @@ __global__ void __launch_bounds__(kColThreads) colsum_kernel(ColsumParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int e = blockIdx.y, col = blockIdx.x * 128 + lane * 4;
     int row0, n;
-    group_rows(p.offsets, p.rows, e, p.st, row0, n);
-    float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
-    if (col < p.N) {
-        int r = warp;
-        for (; r + 8 < n; r += 16) {
-            const float4 a = load4<IN_BF16>(p.dy, (int64_t)(row0 + r) * p.N + col);
-            const float4 b = load4<IN_BF16>(p.dy, (int64_t)(row0 + r + 8) * p.N + col);
-            s0.x += a.x, s0.y += a.y, s0.z += a.z, s0.w += a.w;
-            s1.x += b.x, s1.y += b.y, s1.z += b.z, s1.w += b.w;
+    group_rows(p.offsets, p.rows, e / p.split, p.st, row0, n);
+    if (p.split > 1) part_rows(p.split, e % p.split, row0, n);
+    float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (col < p.N)
+        for (int r = warp; r < n; r += 64) {
+            float4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = r + 8 * i < n ? load4<IN_BF16>(p.dy, (int64_t)(row0 + r + 8 * i) * p.N + col)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                s[i & 1].x += v[i].x;
+                s[i & 1].y += v[i].y;
+                s[i & 1].z += v[i].z;
+                s[i & 1].w += v[i].w;
+            }
         }
-        if (r < n) {
-            const float4 a = load4<IN_BF16>(p.dy, (int64_t)(row0 + r) * p.N + col);
-            s0.x += a.x, s0.y += a.y, s0.z += a.z, s0.w += a.w;
-        }
-    }
-    part[warp][lane] = make_float4(s0.x + s1.x, s0.y + s1.y, s0.z + s1.z, s0.w + s1.w);
+    part[warp][lane] = make_float4(s[0].x + s[1].x, s[0].y + s[1].y, s[0].z + s[1].z, s[0].w + s[1].w);
     __syncthreads();
     if (threadIdx.x < 128) {
         const int c = blockIdx.x * 128 + threadIdx.x;
@@ -295,6 +301,48 @@ __global__ void __launch_bounds__(kColThreads) colsum_kernel(ColsumParams p) {
             if (p.accumulate) v += *d;
             *d = v;
         }
+    }
+}
+
+// ------------------------------------------------------------ parts joined
+// Four neighbouring values per thread; bound by reading the parts, which the kernel before has left in L2.
+template <bool OUT_BF16>
+__global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ part, void* __restrict__ out, int accumulate,
+                                                   int split, int64_t n) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    const float* src = part + (int64_t)blockIdx.y * split * n + i;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int z = 0; z < split; ++z) {
+        const float4 a = *reinterpret_cast<const float4*>(src + z * n);
+        v.x += a.x;
+        v.y += a.y;
+        v.z += a.z;
+        v.w += a.w;
+    }
+    if (OUT_BF16) {
+        uint2* d = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + (int64_t)blockIdx.y * n + i);
+        if (accumulate) {
+            const uint2 o = *d;
+            v.x += bf16_lo(o.x);
+            v.y += bf16_hi(o.x);
+            v.z += bf16_lo(o.y);
+            v.w += bf16_hi(o.y);
+        }
+        *d = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    } else {
+        float4* d = reinterpret_cast<float4*>(static_cast<float*>(out) + (int64_t)blockIdx.y * n + i);
+        if (accumulate) {
+            const float4 o = *d;
+            v.x += o.x;
+            v.y += o.y;
+            v.z += o.z;
+            v.w += o.w;
+        }
+        *d = v;
     }
 }
 
@@ -343,6 +391,8 @@ cudaError_t launch_grouped_gw_f32(const GroupedArgs& a, cudaStream_t s) {
     p.A = static_cast<const float*>(a.x);
     p.B = static_cast<const float*>(a.dy);
     p.out = static_cast<float*>(a.dw);
+    p.E = a.E * a.split;
+    p.split = a.split;
     return launch_form<FORM_GW>(a, p, a.K, a.N, s);
 }
 
@@ -354,11 +404,19 @@ cudaError_t launch_grouped_colsum(const GroupedArgs& a, bool dy_bf16, cudaStream
     p.rows = (int)a.rows;
     p.N = a.N;
     p.accumulate = a.accumulate ? 1 : 0;
+    p.split = a.split;
     p.st = a.st;
-    const dim3 grid((unsigned)((a.N + 127) / 128), (unsigned)a.E), block(kColThreads);
+    const dim3 grid((unsigned)((a.N + 127) / 128), (unsigned)(a.E * a.split)), block(kColThreads);
     if (!dy_bf16) return launch_kernel(colsum_kernel<false, false>, grid, block, 0, s, p);
     return a.out_f32 ? launch_kernel(colsum_kernel<true, false>, grid, block, 0, s, p)
                      : launch_kernel(colsum_kernel<true, true>, grid, block, 0, s, p);
+}
+
+cudaError_t launch_join(const float* part, void* out, bool out_f32, bool accumulate, int E, int split, int64_t n,
+                        cudaStream_t s) {
+    const dim3 grid((unsigned)((n / 4 + 255) / 256), (unsigned)E);
+    return out_f32 ? launch_kernel(join_kernel<false>, grid, dim3(256), 0, s, part, out, accumulate ? 1 : 0, split, n)
+                   : launch_kernel(join_kernel<true>, grid, dim3(256), 0, s, part, out, accumulate ? 1 : 0, split, n);
 }
 
 cudaError_t launch_act_grad_f32(int act, int64_t n, float* g, float* u, float* dh, cudaStream_t s) {

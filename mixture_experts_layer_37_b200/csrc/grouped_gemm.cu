@@ -90,7 +90,8 @@ struct Smem {
 struct GroupedParams {
     const int32_t* offsets = nullptr;  // [E+1]
     int rows = 0;                      // rows of the buffers
-    int E = 0;
+    int E = 0;                         // GW: parts of the experts' rows
+    int split = 1;                     // GW: parts of each expert
     int M = 0;                         // GW: output rows per expert (K of the weights)
     int N = 0;                         // output columns
     int kblocks = 0, kblocks2 = 0;     // FWD, GX: blocks of 64 of the first and of a second operand pair
@@ -336,7 +337,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
     // the prologue above overlaps the launch before; from here on its results are read
     griddep_wait();
     griddep_launch_dependents();
-    if (warp == 2) build_group_tables<kGw>(p.offsets, p.rows, p.E, BM, p.m_tiles, p.st, &tab, lane);
+    if (warp == 2) build_group_tables<kGw>(p.offsets, p.rows, p.E, BM, p.m_tiles, p.st, &tab, lane, kGw ? p.split : 1);
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();  // both CTAs' barriers exist before any cross-CTA signal
@@ -912,16 +913,18 @@ cudaError_t launch_grouped_gw_bf16(const GroupedArgs& a, cudaStream_t s) {
     CUtensorMap mA, mB, mO;
     bool ok = act_map(&mA, a.x, a.rows, a.K, BK);
     ok = ok && act_map(&mB, a.dy, a.rows, a.N, BK);
-    ok = ok && make_map_3d(&mO, a.dw, a.E, a.K, a.N, a.out_f32, a.out_f32 ? 32 : 64, 32);
+    ok = ok && make_map_3d(&mO, a.dw, (int64_t)a.E * a.split, a.K, a.N, a.out_f32, a.out_f32 ? 32 : 64, 32);
     if (!ok) return cudaErrorInvalidValue;
     GroupedParams p = params(a);
+    p.E = a.E * a.split;
+    p.split = a.split;
     p.M = a.K;
     p.N = a.N;
     p.m_tiles = (a.K + BM - 1) / BM;
     p.n_tiles = (a.N + 255) / 256;
     p.out = a.dw;
     p.accumulate = a.accumulate ? 1 : 0;
-    const int64_t tiles = (int64_t)a.E * p.m_tiles * p.n_tiles;
+    const int64_t tiles = (int64_t)p.E * p.m_tiles * p.n_tiles;
     return a.out_f32 ? launch<FORM_GW, EPI_F32>(mA, mB, mA, mB, mO, p, tiles, s)
                      : launch<FORM_GW, EPI_BF16>(mA, mB, mA, mB, mO, p, tiles, s);
 }

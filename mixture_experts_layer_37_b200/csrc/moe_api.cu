@@ -1077,18 +1077,72 @@ cudaError_t grouped_fwd(const GroupedArgs& a, bool bf16, cudaStream_t s) {
 cudaError_t grouped_gx(const GroupedArgs& a, bool bf16, cudaStream_t s) {
     return bf16 ? launch_grouped_gx_bf16(a, s) : launch_grouped_gx_f32(a, s);
 }
-// dW and db; db after dw on the stream.
-cudaError_t grouped_gw(const GroupedArgs& a, bool bf16, cudaStream_t s) {
+
+// Weight and bias gradients whose output is too small to give every SM a tile
+// sum each expert's rows in parts, joined in a fixed order.  The parts of dW:
+// as many as fill the device, none shorter than where a part's own start and
+// the join cost more than they save (bf16: 512 rows; one expert of 8071 rows,
+// 80 x 312: 46 us in one part, see kernels; f32: 128 rows).  Of db: 1024 rows a part.
+constexpr int kPlanSms = 148;
+int gw_split(int64_t rows, int E, int K, int N, bool bf16) {
+    const int64_t per = rows / E, least = bf16 ? 512 : 128;
+    if (per < 4 * least) return 1;
+    const int64_t tiles = bf16 ? (int64_t)E * ((K + 255) / 256) * ((N + 255) / 256) * 2
+                               : (int64_t)E * ((K + 63) / 64) * ((N + 127) / 128);
+    int64_t s = kPlanSms / tiles;
+    if (s > per / least) s = per / least;
+    if (s > kMaxExperts / E) s = kMaxExperts / E;
+    return s > 1 ? (int)s : 1;
+}
+int colsum_split(int64_t rows, int E) {
+    int64_t s = rows / E / 1024;
+    if (s > kMaxExperts / E) s = kMaxExperts / E;
+    return s > 1 ? (int)s : 1;
+}
+// Bytes of the parts of dW, and behind them of db.
+size_t gw_parts_bytes(int64_t rows, int E, int K, int N, bool bf16) {
+    const int s = gw_split(rows, E, K, N, bf16), c = colsum_split(rows, E);
+    return (s > 1 ? align_up((size_t)E * s * K * N * 4, 1024) : 0) + (c > 1 ? align_up((size_t)E * c * N * 4, 1024) : 0);
+}
+
+// dW and db; db after dw on the stream.  parts: gw_parts_bytes.
+cudaError_t grouped_gw(const GroupedArgs& a, bool bf16, uint8_t* parts, cudaStream_t s) {
+    const int split = gw_split(a.rows, a.E, a.K, a.N, bf16), csplit = colsum_split(a.rows, a.E);
+    cudaError_t err = cudaSuccess;
+    GroupedArgs b = a;
     if (a.dw != nullptr) {
-        const cudaError_t err = bf16 ? launch_grouped_gw_bf16(a, s) : launch_grouped_gw_f32(a, s);
+        if (split > 1) {
+            b.split = split;
+            b.dw = parts;
+            b.out_f32 = true;
+            b.accumulate = false;
+        }
+        err = bf16 ? launch_grouped_gw_bf16(b, s) : launch_grouped_gw_f32(b, s);
         if (err != cudaSuccess) return err;
+        if (split > 1) {
+            const PdlScope pdl;
+            err = launch_join(reinterpret_cast<const float*>(parts), a.dw, a.out_f32, a.accumulate, a.E, split,
+                              (int64_t)a.K * a.N, s);
+            if (err != cudaSuccess) return err;
+        }
     }
     if (a.db == nullptr) return cudaSuccess;
-    return launch_grouped_colsum(a, bf16, s);
+    b = a;
+    if (split > 1) parts += align_up((size_t)a.E * split * a.K * a.N * 4, 1024);
+    if (csplit > 1) {
+        b.split = csplit;
+        b.db = parts;
+        b.out_f32 = true;
+        b.accumulate = false;
+    }
+    err = launch_grouped_colsum(b, bf16, s);
+    if (err != cudaSuccess || csplit == 1) return err;
+    const PdlScope pdl;
+    return launch_join(reinterpret_cast<const float*>(parts), a.db, a.out_f32, a.accumulate, a.E, csplit, a.N, s);
 }
 
 struct BackwardPlan {
-    size_t dh, h, d0, d1, total;
+    size_t dh, h, d0, d1, parts, total;
 };
 BackwardPlan backward_plan(const moe_config_t* c) {
     const size_t n = (size_t)max_rows(c) * c->ffn, s = elem_size(c);
@@ -1102,8 +1156,16 @@ BackwardPlan backward_plan(const moe_config_t* c) {
     off = align_up(off + n * s, 1024);
     p.d1 = off;  // gradient of up
     off = align_up(off + (c->act == MOE_ACT_SWIGLU ? n * s : 0), 1024);
-    p.total = off;
+    p.parts = off;  // of the weights' gradients, [E, d, ffn] and [E, ffn, d], one after the other
+    const bool bf16 = c->dtype == MOE_DT_BF16;
+    const size_t in = gw_parts_bytes(max_rows(c), c->E, c->d, c->ffn, bf16);
+    const size_t out = gw_parts_bytes(max_rows(c), c->E, c->ffn, c->d, bf16);
+    p.total = off + (in > out ? in : out);
     return p;
+}
+
+size_t grouped_ws_bytes(const moe_grouped_config_t* g) {
+    return kStatusBytes + gw_parts_bytes(g->rows, g->E, g->K, g->N, g->dtype == MOE_DT_BF16);
 }
 
 }  // namespace
@@ -1114,7 +1176,7 @@ moe_status_t moe_grouped_workspace_size(const moe_grouped_config_t* cfg, size_t*
     const moe_status_t st = check_grouped(cfg);
     if (st != MOE_OK) return st;
     if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
-    *bytes = kStatusBytes;
+    *bytes = grouped_ws_bytes(cfg);
     return MOE_OK;
 }
 
@@ -1124,7 +1186,7 @@ moe_status_t moe_grouped_gemm(const moe_grouped_config_t* cfg, const void* x, co
     if (st != MOE_OK) return st;
     if (!given(w) || offsets == nullptr || !aligned16(bias)) return MOE_ERR_INVALID_ARG;
     if (cfg->rows > 0 && (!given(x) || !given(y))) return MOE_ERR_INVALID_ARG;
-    if ((st = check_grouped_ws(ws, ws_bytes, kStatusBytes)) != MOE_OK) return st;
+    if ((st = check_grouped_ws(ws, ws_bytes, grouped_ws_bytes(cfg))) != MOE_OK) return st;
     if (cfg->rows == 0) return MOE_OK;
     GroupedArgs a = grouped_args(cfg, offsets, ws);
     a.x = x;
@@ -1141,7 +1203,7 @@ moe_status_t moe_grouped_gemm_grad_x(const moe_grouped_config_t* cfg, const void
     if (st != MOE_OK) return st;
     if (!given(w) || offsets == nullptr) return MOE_ERR_INVALID_ARG;
     if (cfg->rows > 0 && (!given(dy) || !given(dx))) return MOE_ERR_INVALID_ARG;
-    if ((st = check_grouped_ws(ws, ws_bytes, kStatusBytes)) != MOE_OK) return st;
+    if ((st = check_grouped_ws(ws, ws_bytes, grouped_ws_bytes(cfg))) != MOE_OK) return st;
     if (cfg->rows == 0) return MOE_OK;
     GroupedArgs a = grouped_args(cfg, offsets, ws);
     a.dy = dy;
@@ -1158,7 +1220,7 @@ moe_status_t moe_grouped_gemm_grad_w(const moe_grouped_config_t* cfg, const void
     if (grad_dtype != MOE_DT_F32 && grad_dtype != cfg->dtype) return MOE_ERR_INVALID_ARG;
     if (!given(dw) || offsets == nullptr || !aligned16(db)) return MOE_ERR_INVALID_ARG;
     if (cfg->rows > 0 && (!given(x) || !given(dy))) return MOE_ERR_INVALID_ARG;
-    if ((st = check_grouped_ws(ws, ws_bytes, kStatusBytes)) != MOE_OK) return st;
+    if ((st = check_grouped_ws(ws, ws_bytes, grouped_ws_bytes(cfg))) != MOE_OK) return st;
     if (cfg->rows == 0) {
         if (accumulate != 0) return MOE_OK;
         const size_t es = grad_dtype == MOE_DT_F32 ? 4 : 2, n = (size_t)cfg->E * cfg->N;
@@ -1173,7 +1235,7 @@ moe_status_t moe_grouped_gemm_grad_w(const moe_grouped_config_t* cfg, const void
     a.db = db;
     a.out_f32 = grad_dtype == MOE_DT_F32;
     a.accumulate = accumulate != 0;
-    return from_cuda(grouped_gw(a, cfg->dtype == MOE_DT_BF16, stream));
+    return from_cuda(grouped_gw(a, cfg->dtype == MOE_DT_BF16, at(ws, kStatusBytes), stream));
 }
 
 static moe_status_t check_int4(const moe_grouped_config_t* g, int32_t group) {
@@ -1209,7 +1271,7 @@ moe_status_t moe_grouped_gemm_int4(const moe_grouped_config_t* cfg, const void* 
     if (cfg->dtype != MOE_DT_BF16) return MOE_ERR_UNSUPPORTED;
     if (!given(codes) || !given(scale) || offsets == nullptr || !aligned16(bias)) return MOE_ERR_INVALID_ARG;
     if (cfg->rows > 0 && (!given(x) || !given(y))) return MOE_ERR_INVALID_ARG;
-    if ((st = check_grouped_ws(ws, ws_bytes, kStatusBytes)) != MOE_OK) return st;
+    if ((st = check_grouped_ws(ws, ws_bytes, grouped_ws_bytes(cfg))) != MOE_OK) return st;
     if (cfg->rows == 0) return MOE_OK;
     GroupedArgs a = grouped_args(cfg, offsets, ws);
     a.x = x;
@@ -1309,16 +1371,16 @@ moe_status_t moe_expert_ffn_backward(const moe_config_t* cfg, const moe_weights_
     out.dy = dy_perm;
     out.dw = grads->w_down_or_w2;
     out.db = db2;
-    if (grouped_gw(out, bf16, stream) != cudaSuccess) return MOE_ERR_CUDA;
+    if (grouped_gw(out, bf16, at(ws, pl.parts), stream) != cudaSuccess) return MOE_ERR_CUDA;
     in.x = x_perm;
     in.dy = d0;
     in.dw = grads->w_gate_or_w1;
     in.db = db1;
-    if (grouped_gw(in, bf16, stream) != cudaSuccess) return MOE_ERR_CUDA;
+    if (grouped_gw(in, bf16, at(ws, pl.parts), stream) != cudaSuccess) return MOE_ERR_CUDA;
     in.dy = d1;
     in.dw = dw_up;
     in.db = nullptr;
-    if (grouped_gw(in, bf16, stream) != cudaSuccess) return MOE_ERR_CUDA;
+    if (grouped_gw(in, bf16, at(ws, pl.parts), stream) != cudaSuccess) return MOE_ERR_CUDA;
     if (grads->dx == nullptr) return MOE_OK;
     // the gradient of the rows; SwiGLU: both pairs in one sum
     a = in;

@@ -62,6 +62,10 @@ SHAPES = [
     ([2] * 64, 0, 256, 128),
     ([0] * 31 + [500] + [0] * 20 + [7] + [0] * 11, 3, 328, 200),
     ([640, 1000], 0, 512, 1024),
+    # long sums of few outputs: the experts' rows in parts
+    ([5000], 3, 72, 136),
+    ([0, 9001, 100, 30], 2, 40, 64),
+    ([2100, 2049, 2200], 0, 264, 72),
 ]
 
 
