@@ -159,6 +159,14 @@ __device__ __forceinline__ int tile_kblocks(const GroupedParams& p, const Tile& 
     return FORM == FORM_GW ? (t.rows + BK - 1) / BK : p.kblocks + p.kblocks2;
 }
 
+// 8 columns of this warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_ld_8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
 // A slab: 32 rows (one per lane) of 128 bytes in shared memory, 16-byte pieces
 // permuted by the row so that both a lane writing its row and eight lanes
 // reading one row touch all banks once.
@@ -660,6 +668,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
             const bool none = tile_kblocks<FORM>(p, t) == 0;  // GW, an expert without rows
             // what the epilogue reads from memory is fetched before the accumulator is waited for
             constexpr bool kGrad = EPI == EPI_SWIGLU_GRAD || EPI == EPI_GELU_GRAD;
+            constexpr int kGradUnroll = EPI == EPI_SWIGLU_GRAD ? 4 : 1;
             constexpr bool kFetch = kGrad || (kGw && EPI == EPI_BF16);
             // SwiGLU: each CTA's 128 columns are [gate 64 | up 64] of the same 64 outputs; a warp takes the
             // 64 outputs of its half (full tile) or 32 of them (half tile)
@@ -692,45 +701,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
                 for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i >> 4][i & 15]);
             };
             if (kGrad) {
-                // dh comes in and h, the gradients go out through the slab, 32 columns at a time
+                // dh comes in and h, the gradients go out through the slab, 32 columns at a time and 8 of them in
+                // registers.  Kept in loops: unrolled over a tile's columns, the activations came to more code than
+                // the instruction caches hold, and a small GELU call took 47 us of which 37 fetched instructions.
                 const int n = EPI == EPI_SWIGLU_GRAD ? ncols / 2 : ncols;
                 const uint32_t ta = EPI == EPI_SWIGLU_GRAD && t.half ? tb - tc0 + 32 * hc : tb;
                 const int g0 = EPI == EPI_SWIGLU_GRAD ? gcol0 : col0;
                 uint8_t* slab = slabs;
-#pragma unroll
-                for (int c = 0; c < (EPI == EPI_SWIGLU_GRAD ? 64 : 128); c += 32) {
+#pragma unroll 1
+                for (int c = 0; c < n && g0 + c < p.N; c += 32) {
                     const int col = g0 + c;
-                    if (c >= n || col >= p.N) break;
-                    put_rows(slab, lane, seen[c / 32 & 1]);
-                    float a[32], u[32], d[32], h[32];
-                    load32(ta + c, a);
-                    if (EPI == EPI_SWIGLU_GRAD) load32(ta + 64 + c, u);
+                    put_rows(slab, lane, seen[0]);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(d + 4 * j) = *slab_piece(slab, lane, j);
-                    if (EPI == EPI_GELU_GRAD) {
-                        if (c < 64) fetch_rows<float>(seen[c / 32 & 1], lane, c + 64 < n ? p.N - (col + 64) : 0, at_col(p.dh, col + 64));
-                        add16_bf16(p.bias + (int64_t)t.e * p.N, col, p.N, a);
-                        add16_bf16(p.bias + (int64_t)t.e * p.N, col + 16, p.N, a + 16);
-                    }
+                    for (int i = 0; i < 8; ++i) seen[0][i] = seen[1][i];
+                    if (c + 64 < n) fetch_rows<float>(seen[1], lane, p.N - (col + 64), at_col(p.dh, col + 64));
+                    uint4 du[4];  // SwiGLU: the gradient of up waits here for the slab
+#pragma unroll kGradUnroll
+                    for (int s = 0; s < 4; ++s) {
+                        uint32_t av[8], uv[8];
+                        tmem_ld_8(ta + c + 8 * s, av);
+                        if (EPI == EPI_SWIGLU_GRAD) tmem_ld_8(ta + 64 + c + 8 * s, uv);
+                        float d[8], h[8], x[8], y[8];
+                        *reinterpret_cast<uint4*>(d) = *slab_piece(slab, lane, 2 * s);
+                        *reinterpret_cast<uint4*>(d + 4) = *slab_piece(slab, lane, 2 * s + 1);
+                        tmem_ld_wait();
+                        if (EPI == EPI_GELU_GRAD) {
+                            const uint4 bv = __ldg(reinterpret_cast<const uint4*>(p.bias + (int64_t)t.e * p.N + col + 8 * s));
+                            const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        if (EPI == EPI_SWIGLU_GRAD)
-                            swiglu_grad(a[i], u[i], d[i], h[i], a[i], u[i]);
-                        else
-                            gelu_grad(a[i], d[i], h[i], a[i]);
-                    }
-                    // pieces 0-3: h, 4-7: the gradient; then the gradient of up
-                    __syncwarp();
+                            for (int i = 0; i < 8; ++i)
+                                x[i] = __uint_as_float(av[i]) + (i & 1 ? bf16_hi(bw[i / 2]) : bf16_lo(bw[i / 2]));
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        *slab_piece(slab, lane, j) = pack8_bf16(h + 8 * j);
-                        *slab_piece(slab, lane, j + 4) = pack8_bf16(a + 8 * j);
+                            for (int i = 0; i < 8; ++i) gelu_grad(x[i], d[i], h[i], x[i]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                swiglu_grad(__uint_as_float(av[i]), __uint_as_float(uv[i]), d[i], h[i], x[i], y[i]);
+                            du[s] = pack8_bf16(y);
+                        }
+                        // into the two pieces just read: h, then the gradient
+                        *slab_piece(slab, lane, 2 * s) = pack8_bf16(h);
+                        *slab_piece(slab, lane, 2 * s + 1) = pack8_bf16(x);
                     }
-                    auto h_row = at_col(p.h, col), g_row = at_col(p.d0, col - 32);
-                    store_slab<__nv_bfloat16>(slab, lane, 64, [&](int r) { return (lane & 7) < 4 ? h_row(r) : g_row(r); });
+                    auto h_row = at_col(p.h, col), g_row = at_col(p.d0, col);
+                    const int piece = lane & 7, shift = (piece >> 1) * 8 - piece * 8;  // columns of a piece; the slab's own
+                    store_slab<__nv_bfloat16>(slab, lane, 64, [&](int r) {
+                        __nv_bfloat16* o = piece & 1 ? g_row(r) : h_row(r);
+                        return o != nullptr ? o + shift : nullptr;
+                    });
                     if (EPI == EPI_SWIGLU_GRAD) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) *slab_piece(slab, lane, j) = pack8_bf16(u + 8 * j);
+                        for (int j = 0; j < 4; ++j) *slab_piece(slab, lane, j) = du[j];
                         store_slab<__nv_bfloat16>(slab, lane, 32, at_col(p.d1, col));
                     }
                 }
