@@ -134,7 +134,8 @@ cudaError_t launch_quantize_int4(const void* w, bool bf16, const int8_t* given, 
 cudaError_t launch_join(const float* part, void* out, bool out_f32, bool accumulate, int E, int split, int64_t n,
                         cudaStream_t s);
 // db[e,n] (+)= sum over the rows of e of dy[r,n]; db in fp32 (a.out_f32) or bf16.
-cudaError_t launch_grouped_colsum(const GroupedArgs& a, bool dy_bf16, cudaStream_t s);
+// `also` (or null): a second one in the same launch, for the same rows and with the same options.
+cudaError_t launch_grouped_colsum(const GroupedArgs& a, const GroupedArgs* also, bool dy_bf16, cudaStream_t s);
 // Elementwise over all rows in fp32: from g, u and dh to h (over dh), dg (over g), du (over u).
 cudaError_t launch_act_grad_f32(int act, int64_t n, float* g, float* u, float* dh, cudaStream_t s);
 

@@ -234,13 +234,18 @@ F32Params params(const GroupedArgs& a) {
 }
 
 // ------------------------------------------------------------ bias gradients
-constexpr int kColThreads = 256;  // 8 warps; a lane holds 4 columns
+constexpr int kColWarps = 16;  // a lane holds 4 columns
 
+struct ColsumJob {
+    const void* dy = nullptr;  // [rows, N]
+    void* db = nullptr;        // [E, N], or [E, split, N]
+    int N = 0;
+};
 struct ColsumParams {
-    const void* dy = nullptr;
-    void* db = nullptr;
+    ColsumJob job[2];
+    int tiles0 = 0;  // tiles of 128 columns of the first job; the second's follow
     const int32_t* offsets = nullptr;
-    int rows = 0, N = 0, accumulate = 0, split = 1;
+    int rows = 0, accumulate = 0, split = 1;
     DevStatus st;
 };
 
@@ -254,27 +259,29 @@ __device__ __forceinline__ float4 load4(const void* base, int64_t i) {
 }
 
 // One CTA per (expert or part of its rows, 128 columns): warp w adds the rows w,
-// w+8, ... in two interleaved sums, eight rows loaded at a time (the loads'
-// latency bounds this kernel), and the sixteen sums of a column are added in a
-// fixed order.
+// w+16, ... in two interleaved sums, eight rows loaded at a time (the loads'
+// latency bounds this kernel), and the warps' sums are added in a fixed order.
 template <bool IN_BF16, bool OUT_BF16>
-__global__ void __launch_bounds__(kColThreads) colsum_kernel(ColsumParams p) {
-    __shared__ float4 part[8][32];
+__global__ void __launch_bounds__(kColWarps * 32) colsum_kernel(ColsumParams p) {
+    __shared__ float4 part[kColWarps][32];
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int e = blockIdx.y, col = blockIdx.x * 128 + lane * 4;
+    const bool second = (int)blockIdx.x >= p.tiles0;
+    const ColsumJob j = second ? p.job[1] : p.job[0];
+    const int n0 = (blockIdx.x - (second ? p.tiles0 : 0)) * 128;
+    const int e = blockIdx.y, col = n0 + lane * 4;
     int row0, n;
     group_rows(p.offsets, p.rows, e / p.split, p.st, row0, n);
     if (p.split > 1) part_rows(p.split, e % p.split, row0, n);
     float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-    if (col < p.N)
-        for (int r = warp; r < n; r += 64) {
+    if (col < j.N)
+        for (int r = warp; r < n; r += 8 * kColWarps) {
             float4 v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                v[i] = r + 8 * i < n ? load4<IN_BF16>(p.dy, (int64_t)(row0 + r + 8 * i) * p.N + col)
-                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[i] = r + kColWarps * i < n ? load4<IN_BF16>(j.dy, (int64_t)(row0 + r + kColWarps * i) * j.N + col)
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 s[i & 1].x += v[i].x;
@@ -286,18 +293,18 @@ __global__ void __launch_bounds__(kColThreads) colsum_kernel(ColsumParams p) {
     part[warp][lane] = make_float4(s[0].x + s[1].x, s[0].y + s[1].y, s[0].z + s[1].z, s[0].w + s[1].w);
     __syncthreads();
     if (threadIdx.x < 128) {
-        const int c = blockIdx.x * 128 + threadIdx.x;
-        if (c >= p.N) return;
+        const int c = n0 + threadIdx.x;
+        if (c >= j.N) return;
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) v += reinterpret_cast<const float*>(part[w])[threadIdx.x];
-        const int64_t o = (int64_t)e * p.N + c;
+        for (int w = 0; w < kColWarps; ++w) v += reinterpret_cast<const float*>(part[w])[threadIdx.x];
+        const int64_t o = (int64_t)e * j.N + c;
         if (OUT_BF16) {
-            __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.db) + o;
+            __nv_bfloat16* d = static_cast<__nv_bfloat16*>(j.db) + o;
             if (p.accumulate) v += __bfloat162float(*d);
             *d = __float2bfloat16_rn(v);
         } else {
-            float* d = static_cast<float*>(p.db) + o;
+            float* d = static_cast<float*>(j.db) + o;
             if (p.accumulate) v += *d;
             *d = v;
         }
@@ -396,17 +403,23 @@ cudaError_t launch_grouped_gw_f32(const GroupedArgs& a, cudaStream_t s) {
     return launch_form<FORM_GW>(a, p, a.K, a.N, s);
 }
 
-cudaError_t launch_grouped_colsum(const GroupedArgs& a, bool dy_bf16, cudaStream_t s) {
+cudaError_t launch_grouped_colsum(const GroupedArgs& a, const GroupedArgs* also, bool dy_bf16, cudaStream_t s) {
     ColsumParams p;
-    p.dy = a.dy;
-    p.db = a.db;
+    int tiles = 0;
+    for (int i = 0; i < (also != nullptr ? 2 : 1); ++i) {
+        const GroupedArgs& g = i == 0 ? a : *also;
+        p.job[i].dy = g.dy;
+        p.job[i].db = g.db;
+        p.job[i].N = g.N;
+        tiles += (g.N + 127) / 128;
+        if (i == 0) p.tiles0 = tiles;
+    }
     p.offsets = a.offsets;
     p.rows = (int)a.rows;
-    p.N = a.N;
     p.accumulate = a.accumulate ? 1 : 0;
     p.split = a.split;
     p.st = a.st;
-    const dim3 grid((unsigned)((a.N + 127) / 128), (unsigned)(a.E * a.split)), block(kColThreads);
+    const dim3 grid((unsigned)tiles, (unsigned)(a.E * a.split)), block(kColWarps * 32);
     if (!dy_bf16) return launch_kernel(colsum_kernel<false, false>, grid, block, 0, s, p);
     return a.out_f32 ? launch_kernel(colsum_kernel<true, false>, grid, block, 0, s, p)
                      : launch_kernel(colsum_kernel<true, true>, grid, block, 0, s, p);

@@ -716,6 +716,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
                     for (int i = 0; i < 8; ++i) seen[0][i] = seen[1][i];
                     if (c + 64 < n) fetch_rows<float>(seen[1], lane, p.N - (col + 64), at_col(p.dh, col + 64));
                     uint4 du[4];  // SwiGLU: the gradient of up waits here for the slab
+                    uint4 bias[4];
+                    if (EPI == EPI_GELU_GRAD) {
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            bias[s] = __ldg(reinterpret_cast<const uint4*>(p.bias + (int64_t)t.e * p.N + col) + s);
+                    }
 #pragma unroll kGradUnroll
                     for (int s = 0; s < 4; ++s) {
                         uint32_t av[8], uv[8];
@@ -726,13 +732,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
                         *reinterpret_cast<uint4*>(d + 4) = *slab_piece(slab, lane, 2 * s + 1);
                         tmem_ld_wait();
                         if (EPI == EPI_GELU_GRAD) {
-                            const uint4 bv = __ldg(reinterpret_cast<const uint4*>(p.bias + (int64_t)t.e * p.N + col + 8 * s));
-                            const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
+                            const uint32_t bw[4] = {bias[0].x, bias[0].y, bias[0].z, bias[0].w};
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
                                 x[i] = __uint_as_float(av[i]) + (i & 1 ? bf16_hi(bw[i / 2]) : bf16_lo(bw[i / 2]));
 #pragma unroll
                             for (int i = 0; i < 8; ++i) gelu_grad(x[i], d[i], h[i], x[i]);
+                            bias[0] = bias[1];
+                            bias[1] = bias[2];
+                            bias[2] = bias[3];
                         } else {
 #pragma unroll
                             for (int i = 0; i < 8; ++i)

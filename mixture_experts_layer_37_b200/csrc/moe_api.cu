@@ -1099,46 +1099,53 @@ int colsum_split(int64_t rows, int E) {
     if (s > kMaxExperts / E) s = kMaxExperts / E;
     return s > 1 ? (int)s : 1;
 }
-// Bytes of the parts of dW, and behind them of db.
 size_t gw_parts_bytes(int64_t rows, int E, int K, int N, bool bf16) {
-    const int s = gw_split(rows, E, K, N, bf16), c = colsum_split(rows, E);
-    return (s > 1 ? align_up((size_t)E * s * K * N * 4, 1024) : 0) + (c > 1 ? align_up((size_t)E * c * N * 4, 1024) : 0);
+    const int s = gw_split(rows, E, K, N, bf16);
+    return s > 1 ? align_up((size_t)E * s * K * N * 4, 1024) : 0;
+}
+size_t colsum_parts_bytes(int64_t rows, int E, int N) {
+    const int s = colsum_split(rows, E);
+    return s > 1 ? align_up((size_t)E * s * N * 4, 1024) : 0;
 }
 
-// dW and db; db after dw on the stream.  parts: gw_parts_bytes.
+// dW.  parts: gw_parts_bytes.
 cudaError_t grouped_gw(const GroupedArgs& a, bool bf16, uint8_t* parts, cudaStream_t s) {
-    const int split = gw_split(a.rows, a.E, a.K, a.N, bf16), csplit = colsum_split(a.rows, a.E);
-    cudaError_t err = cudaSuccess;
+    if (a.dw == nullptr) return cudaSuccess;
     GroupedArgs b = a;
-    if (a.dw != nullptr) {
-        if (split > 1) {
-            b.split = split;
-            b.dw = parts;
-            b.out_f32 = true;
-            b.accumulate = false;
-        }
-        err = bf16 ? launch_grouped_gw_bf16(b, s) : launch_grouped_gw_f32(b, s);
-        if (err != cudaSuccess) return err;
-        if (split > 1) {
-            const PdlScope pdl;
-            err = launch_join(reinterpret_cast<const float*>(parts), a.dw, a.out_f32, a.accumulate, a.E, split,
-                              (int64_t)a.K * a.N, s);
-            if (err != cudaSuccess) return err;
-        }
-    }
-    if (a.db == nullptr) return cudaSuccess;
-    b = a;
-    if (split > 1) parts += align_up((size_t)a.E * split * a.K * a.N * 4, 1024);
-    if (csplit > 1) {
-        b.split = csplit;
-        b.db = parts;
+    b.split = gw_split(a.rows, a.E, a.K, a.N, bf16);
+    if (b.split > 1) {
+        b.dw = parts;
         b.out_f32 = true;
         b.accumulate = false;
     }
-    err = launch_grouped_colsum(b, bf16, s);
-    if (err != cudaSuccess || csplit == 1) return err;
+    const cudaError_t err = bf16 ? launch_grouped_gw_bf16(b, s) : launch_grouped_gw_f32(b, s);
+    if (err != cudaSuccess || b.split == 1) return err;
     const PdlScope pdl;
-    return launch_join(reinterpret_cast<const float*>(parts), a.db, a.out_f32, a.accumulate, a.E, csplit, a.N, s);
+    return launch_join(reinterpret_cast<const float*>(parts), a.dw, a.out_f32, a.accumulate, a.E, b.split,
+                       (int64_t)a.K * a.N, s);
+}
+
+// db, and that of `also` (or null) in the same launch.  parts: colsum_parts_bytes for each.
+cudaError_t grouped_db(const GroupedArgs& a, const GroupedArgs* also, bool bf16, uint8_t* parts, cudaStream_t s) {
+    if (a.db == nullptr) return also != nullptr && also->db != nullptr ? grouped_db(*also, nullptr, bf16, parts, s) : cudaSuccess;
+    if (also != nullptr && also->db == nullptr) also = nullptr;
+    const int split = colsum_split(a.rows, a.E);
+    GroupedArgs b = a, c = also != nullptr ? *also : a;
+    uint8_t* const second = parts + colsum_parts_bytes(a.rows, a.E, a.N);
+    if (split > 1) {
+        b.split = c.split = split;
+        b.db = parts;
+        c.db = second;
+        b.out_f32 = c.out_f32 = true;
+        b.accumulate = c.accumulate = false;
+    }
+    cudaError_t err = launch_grouped_colsum(b, also != nullptr ? &c : nullptr, bf16, s);
+    if (err != cudaSuccess || split == 1) return err;
+    const PdlScope pdl;
+    err = launch_join(reinterpret_cast<const float*>(parts), a.db, a.out_f32, a.accumulate, a.E, split, a.N, s);
+    if (err != cudaSuccess || also == nullptr) return err;
+    return launch_join(reinterpret_cast<const float*>(second), also->db, also->out_f32, also->accumulate, a.E, split, also->N,
+                       s);
 }
 
 struct BackwardPlan {
@@ -1156,16 +1163,20 @@ BackwardPlan backward_plan(const moe_config_t* c) {
     off = align_up(off + n * s, 1024);
     p.d1 = off;  // gradient of up
     off = align_up(off + (c->act == MOE_ACT_SWIGLU ? n * s : 0), 1024);
-    p.parts = off;  // of the weights' gradients, [E, d, ffn] and [E, ffn, d], one after the other
+    p.parts = off;  // of the gradients of one [E, d, ffn] or [E, ffn, d], and of b1 and b2, one after the other
     const bool bf16 = c->dtype == MOE_DT_BF16;
-    const size_t in = gw_parts_bytes(max_rows(c), c->E, c->d, c->ffn, bf16);
-    const size_t out = gw_parts_bytes(max_rows(c), c->E, c->ffn, c->d, bf16);
-    p.total = off + (in > out ? in : out);
+    const int64_t rows = max_rows(c);
+    size_t most = gw_parts_bytes(rows, c->E, c->d, c->ffn, bf16);
+    for (size_t n : {gw_parts_bytes(rows, c->E, c->ffn, c->d, bf16),
+                     colsum_parts_bytes(rows, c->E, c->ffn) + colsum_parts_bytes(rows, c->E, c->d)})
+        most = n > most ? n : most;
+    p.total = off + most;
     return p;
 }
 
 size_t grouped_ws_bytes(const moe_grouped_config_t* g) {
-    return kStatusBytes + gw_parts_bytes(g->rows, g->E, g->K, g->N, g->dtype == MOE_DT_BF16);
+    return kStatusBytes + gw_parts_bytes(g->rows, g->E, g->K, g->N, g->dtype == MOE_DT_BF16) +
+           colsum_parts_bytes(g->rows, g->E, g->N);
 }
 
 }  // namespace
@@ -1235,7 +1246,12 @@ moe_status_t moe_grouped_gemm_grad_w(const moe_grouped_config_t* cfg, const void
     a.db = db;
     a.out_f32 = grad_dtype == MOE_DT_F32;
     a.accumulate = accumulate != 0;
-    return from_cuda(grouped_gw(a, cfg->dtype == MOE_DT_BF16, at(ws, kStatusBytes), stream));
+    const bool bf16 = cfg->dtype == MOE_DT_BF16;
+    const cudaError_t err = grouped_gw(a, bf16, at(ws, kStatusBytes), stream);
+    if (err != cudaSuccess || db == nullptr) return from_cuda(err);
+    const PdlScope pdl;
+    const size_t off = kStatusBytes + gw_parts_bytes(cfg->rows, cfg->E, cfg->K, cfg->N, bf16);
+    return from_cuda(grouped_db(a, nullptr, bf16, at(ws, off), stream));
 }
 
 static moe_status_t check_int4(const moe_grouped_config_t* g, int32_t group) {
@@ -1377,6 +1393,7 @@ moe_status_t moe_expert_ffn_backward(const moe_config_t* cfg, const moe_weights_
     in.dw = grads->w_gate_or_w1;
     in.db = db1;
     if (grouped_gw(in, bf16, at(ws, pl.parts), stream) != cudaSuccess) return MOE_ERR_CUDA;
+    if (grouped_db(in, &out, bf16, at(ws, pl.parts), stream) != cudaSuccess) return MOE_ERR_CUDA;
     in.dy = d1;
     in.dw = dw_up;
     in.db = nullptr;
