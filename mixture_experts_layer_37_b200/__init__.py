@@ -679,6 +679,11 @@ class GroupedConfig:
         object.__setattr__(self, "_c", MoEGroupedConfigC(self.rows, self.E, self.K, self.N,
                                                          MOE_DT_BF16 if self.dtype == "bf16" else MOE_DT_F32))
         object.__setattr__(self, "_ref", ctypes.byref(self._c))
+        E, K, N, dt = self.E, self.K, self.N, (self.torch_dtype,)
+        gdt = (self.torch_dtype, torch.float32)
+        for name, shape, dts in (("_x", (self.rows, K), dt), ("_y", (self.rows, N), dt), ("_w", (E, K, N), dt),
+                                 ("_b", (E, N), dt), ("_o", (E + 1,), (torch.int32,)), ("_dw", (E, K, N), gdt)):
+            object.__setattr__(self, name, (torch.Size(shape) if min(shape) >= 0 else shape, dts))
 
     def c(self) -> MoEGroupedConfigC:
         return self._c
@@ -699,19 +704,38 @@ def _fn(name: str, *argtypes):
     return f
 
 
+def _refuse(where: str, t, shape, dtypes, device):
+    raise MoEError(MOE_ERR_INVALID_ARG, f"{where}: a contiguous tensor {list(shape)} of {dtypes} on {device} is wanted, "
+                                        f"got {list(t.shape)} {t.dtype} on {t.device}")
+
+
+def _given(where: str, index: int, device, t, want) -> int:
+    """The address of t, a contiguous tensor on CUDA device `index` of the shape and
+    one of the types in `want` (0 for None and for an empty tensor)."""
+    if t is None:
+        return 0
+    shape, dtypes = want
+    if t.shape != shape or t.dtype not in dtypes or t.get_device() != index or not t.is_contiguous():
+        _refuse(where, t, shape, dtypes, device)
+    return t.data_ptr()
+
+
 def _expect(where: str, device, *specs) -> None:
     """Each (tensor or None, shape, dtypes): a contiguous tensor on `device`."""
+    index = _cuda_index(where, device)
     for t, shape, dtypes in specs:
-        if t is not None and (t.shape != shape or t.dtype not in dtypes or t.device != device or not t.is_contiguous()):
-            raise MoEError(MOE_ERR_INVALID_ARG, f"{where}: a contiguous tensor {list(shape)} of {dtypes} on {device} "
-                                                f"is wanted, got {list(t.shape)} {t.dtype} on {t.device}")
+        _given(where, index, device, t, (shape, dtypes))
+
+
+def _cuda_index(where: str, device) -> int:
+    if device.type != "cuda":
+        raise MoEError(MOE_ERR_INVALID_ARG, f"{where}: tensors on a CUDA device are wanted, got {device}")
+    return device.index
 
 
 def _call_on(device, name: str, f, args, stream) -> None:
     """f(*args, stream) with `device` current (its current stream where none is given)."""
     index = device.index
-    if device.type != "cuda":
-        raise MoEError(MOE_ERR_INVALID_ARG, f"{name}: tensors on a CUDA device are wanted, got {device}")
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(index)
     elif hasattr(stream, "cuda_stream"):
@@ -738,36 +762,36 @@ def moe_grouped_workspace_size(g: GroupedConfig) -> int:
 
 def moe_grouped_gemm(g: GroupedConfig, x, w, offsets, y, ws: Workspace, bias=None, stream=None) -> None:
     """y[r] = x[r] w[e] (+ bias[e]) for the rows r in [offsets[e], offsets[e+1])."""
-    dt = (g.torch_dtype,)
-    _expect("moe_grouped_gemm", w.device, (x, (g.rows, g.K), dt), (w, (g.E, g.K, g.N), dt), (y, (g.rows, g.N), dt),
-            (bias, (g.E, g.N), dt), (offsets, (g.E + 1,), (torch.int32,)))
+    name, dev = "moe_grouped_gemm", w.device
+    i = _cuda_index(name, dev)
+    args = (g._ref, _given(name, i, dev, x, g._x), _given(name, i, dev, w, g._w), _given(name, i, dev, bias, g._b),
+            _given(name, i, dev, offsets, g._o), _given(name, i, dev, y, g._y), ws.ptr, ws.nbytes)
     f = _fn("moe_grouped_gemm", _GCFG, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P)
-    _call_on(w.device, "moe_grouped_gemm", f, (g._ref, _ptr(x), _ptr(w), _ptr(bias), _ptr(offsets),
-                                               _ptr(y), ws.ptr, ws.nbytes), stream)
+    _call_on(dev, name, f, args, stream)
 
 
 def moe_grouped_gemm_grad_x(g: GroupedConfig, dy, w, offsets, dx, ws: Workspace, stream=None) -> None:
     """dx[r] = dy[r] w[e]^T for the rows r in [offsets[e], offsets[e+1])."""
-    dt = (g.torch_dtype,)
-    _expect("moe_grouped_gemm_grad_x", w.device, (dy, (g.rows, g.N), dt), (w, (g.E, g.K, g.N), dt),
-            (dx, (g.rows, g.K), dt), (offsets, (g.E + 1,), (torch.int32,)))
+    name, dev = "moe_grouped_gemm_grad_x", w.device
+    i = _cuda_index(name, dev)
+    args = (g._ref, _given(name, i, dev, dy, g._y), _given(name, i, dev, w, g._w), _given(name, i, dev, offsets, g._o),
+            _given(name, i, dev, dx, g._x), ws.ptr, ws.nbytes)
     f = _fn("moe_grouped_gemm_grad_x", _GCFG, _P, _P, _P, _P, _P, ctypes.c_size_t, _P)
-    _call_on(w.device, "moe_grouped_gemm_grad_x", f, (g._ref, _ptr(dy), _ptr(w), _ptr(offsets), _ptr(dx),
-                                                      ws.ptr, ws.nbytes), stream)
+    _call_on(dev, name, f, args, stream)
 
 
 def moe_grouped_gemm_grad_w(g: GroupedConfig, x, dy, offsets, dw, ws: Workspace, db=None, accumulate: bool = False,
                             stream=None) -> None:
     """dw[e] = x_e^T dy_e and db[e] = sum of dy_e over the rows of e, added to
     what is there with `accumulate`; dw and db in g's dtype or float32."""
-    dt, gdt = (g.torch_dtype,), {g.torch_dtype, torch.float32}
-    _expect("moe_grouped_gemm_grad_w", dw.device, (x, (g.rows, g.K), dt), (dy, (g.rows, g.N), dt),
-            (dw, (g.E, g.K, g.N), gdt), (db, (g.E, g.N), (dw.dtype,)), (offsets, (g.E + 1,), (torch.int32,)))
+    name, dev = "moe_grouped_gemm_grad_w", dw.device
+    i = _cuda_index(name, dev)
+    args = (g._ref, _given(name, i, dev, x, g._x), _given(name, i, dev, dy, g._y), _given(name, i, dev, offsets, g._o),
+            _given(name, i, dev, dw, g._dw), _given(name, i, dev, db, (g._b[0], (dw.dtype,))), _dtype_code(dw.dtype),
+            1 if accumulate else 0, ws.ptr, ws.nbytes)
     f = _fn("moe_grouped_gemm_grad_w", _GCFG, _P, _P, _P, _P, _P, ctypes.c_int32, ctypes.c_int32, _P, ctypes.c_size_t,
             _P)
-    _call_on(dw.device, "moe_grouped_gemm_grad_w", f,
-             (g._ref, _ptr(x), _ptr(dy), _ptr(offsets), _ptr(dw), _ptr(db), _dtype_code(dw.dtype),
-              1 if accumulate else 0, ws.ptr, ws.nbytes), stream)
+    _call_on(dev, name, f, args, stream)
 
 
 def moe_expert_ffn_backward_workspace_size(cfg: MoEConfig) -> int:
@@ -841,12 +865,11 @@ def moe_pack_int4(q: torch.Tensor, stream=None) -> torch.Tensor:
 def moe_grouped_gemm_int4(g: GroupedConfig, x, codes, scale, offsets, y, ws: Workspace, group: int, bias=None,
                           stream=None) -> None:
     """y[r] = x[r] W[e] (+ bias[e]) with W as 4-bit codes and per-group scales."""
-    dt = (g.torch_dtype,)
+    name, dev = "moe_grouped_gemm_int4", codes.device
+    i = _cuda_index(name, dev)
     cs, ss = _int4_shapes(g.E, g.K, g.N, max(int(group), 1))
-    _expect("moe_grouped_gemm_int4", codes.device, (x, (g.rows, g.K), dt), (codes, cs, (torch.uint8,)),
-            (scale, ss, (torch.float32,)), (y, (g.rows, g.N), dt), (bias, (g.E, g.N), dt),
-            (offsets, (g.E + 1,), (torch.int32,)))
+    args = (g._ref, _given(name, i, dev, x, g._x), _given(name, i, dev, codes, (cs, (torch.uint8,))),
+            _given(name, i, dev, scale, (ss, (torch.float32,))), int(group), _given(name, i, dev, bias, g._b),
+            _given(name, i, dev, offsets, g._o), _given(name, i, dev, y, g._y), ws.ptr, ws.nbytes)
     f = _fn("moe_grouped_gemm_int4", _GCFG, _P, _P, _P, ctypes.c_int32, _P, _P, _P, _P, ctypes.c_size_t, _P)
-    _call_on(codes.device, "moe_grouped_gemm_int4", f,
-             (g._ref, _ptr(x), _ptr(codes), _ptr(scale), int(group), _ptr(bias), _ptr(offsets), _ptr(y),
-              ws.ptr, ws.nbytes), stream)
+    _call_on(dev, name, f, args, stream)
