@@ -236,7 +236,6 @@ template <int N>
 __device__ __forceinline__ void tma_store_wait_read() {
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void tma_store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // mbar_wait_bounded for a phase that the other CTA's threads complete after
 // writing its shared memory: acquires at cluster scope.
@@ -818,7 +817,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
             }
             if (!none) release();
         }
-        if (lane == 0) tma_store_wait_all();
+        // the stores have read their slabs; what they write is complete with the grid
+        if (lane == 0) tma_store_wait_read<0>();
         __syncwarp();
     }
     tc_fence_before();

@@ -333,6 +333,8 @@ FFN_CASES = [
     ("swiglu", "f32", [30, 0, 70], 3, 36, 20),
     ("gelu_bias", "bf16", [70, 0, 130, 1], 6, 192, 320),
     ("gelu_bias", "f32", [33, 1, 0], 2, 68, 100),
+    ("gelu_bias", "bf16", [2100, 3000], 2, 64, 128),   # biases and matrices summed in parts
+    ("swiglu", "f32", [1200], 0, 32, 64),
 ]
 
 
