@@ -237,6 +237,13 @@ __device__ __forceinline__ void tma_store_wait_read() {
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
+// mbar_arrive_cluster without releasing this thread's writes.  For "accumulator read": the reads are done
+// (tcgen05.wait::ld) and ordered by the tcgen05 fence, and whoever waits reads nothing that this thread wrote,
+// while a releasing arrival waits for the tile's own global stores (1,850 clocks in a one-tile call).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // mbar_wait_bounded for a phase that the other CTA's threads complete after
 // writing its shared memory: acquires at cluster scope.
 __device__ __forceinline__ bool mbar_wait_bounded_cluster(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
@@ -256,22 +263,7 @@ __device__ __forceinline__ bool mbar_wait_bounded_cluster(uint64_t* bar, uint32_
     }
 }
 
-// x += 16 bf16 values at row + col (those inside N).
-__device__ __forceinline__ void add16_bf16(const __nv_bfloat16* row, int col, int N, float* x) {
-#pragma unroll
-    for (int hlf = 0; hlf < 2; ++hlf)
-        if (col + 8 * hlf < N) {
-            const uint4 b = *reinterpret_cast<const uint4*>(row + col + 8 * hlf);
-            const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[8 * hlf + 2 * i] += bf16_lo(w[i]);
-                x[8 * hlf + 2 * i + 1] += bf16_hi(w[i]);
-            }
-        }
-}
-
-// The activation's backward pass for 16 columns of one row, from the fp32
+// The activation's backward pass, from the fp32
 // accumulators of its own products and the fp32 gradient dh.  Only what the
 // next products read is rounded to bf16 (their operand type), once.
 //   SwiGLU  s = sigmoid(g): h = g s u, dg = dh u s (1 + g (1 - s)), du = dh g s
@@ -560,7 +552,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
         auto release = [&]() {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(tempty_lead + 8u * acc);
+            if (lane == 0) mbar_arrive_cluster_relaxed(tempty_lead + 8u * acc);
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
         };
@@ -683,6 +675,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
                     }
                 }
             }
+            uint2 bias = make_uint2(0, 0);  // FWD: lane i holds the bias of the warp's columns 4i..4i+3
+            if (FORM == FORM_FWD && EPI == EPI_BF16 && p.bias != nullptr && col0 + 4 * lane < p.N)
+                bias = __ldg(reinterpret_cast<const uint2*>(p.bias + (int64_t)t.e * p.N + col0 + 4 * lane));
             if (kGrad) {
                 const int g0 = EPI == EPI_SWIGLU_GRAD ? gcol0 : col0;
 #pragma unroll
@@ -764,10 +759,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
                 }
             } else {
                 constexpr int kCols = EPI == EPI_F32 ? 32 : 64;  // columns of a slab
-#pragma unroll
-                for (int c = 0; c < 128; c += kCols) {
+                // not unrolled: a call of one tile fetches every instruction that it executes
+#pragma unroll 1
+                for (int c = 0; c < ncols; c += kCols) {
                     const int col = col0 + c;
-                    if (c >= ncols || col >= p.N || rn <= 0 || (none && p.accumulate)) break;
+                    if (col >= p.N || rn <= 0 || (none && p.accumulate)) break;
                     float x[kCols];
                     if (none) {
 #pragma unroll
@@ -777,9 +773,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
                         if (kCols == 64) load32(tb + c + 32, x + 32);
                     }
                     uint8_t* slab = next_slab();
-                    if (FORM == FORM_FWD && p.bias != nullptr) {
+                    if (FORM == FORM_FWD && EPI == EPI_BF16 && p.bias != nullptr) {
 #pragma unroll
-                        for (int i = 0; i < kCols; i += 16) add16_bf16(p.bias + (int64_t)t.e * p.N, col + i, p.N, x + i);
+                        for (int i = 0; i < kCols / 4; ++i) {
+                            const uint32_t b0 = __shfl_sync(0xffffffffu, bias.x, c / 4 + i);
+                            const uint32_t b1 = __shfl_sync(0xffffffffu, bias.y, c / 4 + i);
+                            x[4 * i] += bf16_lo(b0);
+                            x[4 * i + 1] += bf16_hi(b0);
+                            x[4 * i + 2] += bf16_lo(b1);
+                            x[4 * i + 3] += bf16_hi(b1);
+                        }
                     }
                     if (EPI == EPI_F32) {
 #pragma unroll
@@ -787,7 +790,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
                     } else {
                         if (kGw && p.accumulate) {
                             // what is there, through the slab; added in fp32, one rounding
-                            put_rows(slab, lane, seen[c / 64 & 1]);
+                            put_rows(slab, lane, seen[0]);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) seen[0][i] = seen[kFetch ? 1 : 0][i];
 #pragma unroll
                             for (int j = 0; j < kCols / 8; ++j) {
                                 const uint4 v = *slab_piece(slab, lane, j);
