@@ -239,6 +239,10 @@ moe_status_t check_weights(const moe_config_t* c, const moe_weights_t* w, bool n
             (w->gate_or_w1_scale == nullptr || w->down_or_w2_scale == nullptr ||
              (c->act == MOE_ACT_SWIGLU && w->up_scale == nullptr)))
             return MOE_ERR_INVALID_ARG;
+        // 4-bit: the scales are read by TMA
+        if (int4_group(c->weight_format) != 0 &&
+            (!aligned16(w->gate_or_w1_scale) || !aligned16(w->up_scale) || !aligned16(w->down_or_w2_scale)))
+            return MOE_ERR_INVALID_ARG;
         if (c->n_shared > 0) {
             if (w->shared_gate_or_w1 == nullptr || w->shared_down_or_w2 == nullptr ||
                 !aligned16(w->shared_gate_or_w1) || !aligned16(w->shared_down_or_w2))
@@ -1258,7 +1262,9 @@ static moe_status_t check_int4(const moe_grouped_config_t* g, int32_t group) {
     const moe_status_t st = check_grouped(g);
     if (st != MOE_OK) return st;
     if (int4_group(group) == 0) return MOE_ERR_INVALID_ARG;
-    if (g->K > kMaxInt4K || (int64_t)g->E * g->N >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+    const int64_t tiles = (g->rows / 16 + g->E) * ((g->N + 127) / 128);  // and two-block stages of a tile: 32 bits
+    if (g->K > kMaxInt4K || (int64_t)g->E * g->N >= ((int64_t)1 << 31) || tiles * ((g->K + 255) / 256) >= ((int64_t)1 << 31))
+        return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 

@@ -240,3 +240,87 @@ def test_layer_forward_captured_on_another_stream_and_again():
     o2 = torch.zeros_like(x)
     M.moe_combine(cfg, y_perm, out["slot"], out["topk_w"], o2)
     assert torch.equal(o2, first)
+
+
+def test_expert_parallel_ranks_equal_the_whole_batch():
+    """Two emulated expert-parallel ranks on 4-bit experts: bit for bit one forward over the batch (tiles of 16
+    tokens or 64 sum each output in the same order)."""
+    import workloads as W
+    from test_gpu_ep import run_emulated
+    from gpu_common import to_dev, weights_dev
+    wl = W.Workload("ep_int4", T=190, d=128, ffn=192, E=4, k=2, act="swiglu", dtype="bf16", capacity_factor=1.0, seed=61,
+                    weights="int4_g32")
+    inp = W.make_inputs(wl)
+    cfg = M.MoEConfig.of(wl)
+    wd = M.quantize_expert_weights(cfg, weights_dev(wl, inp))
+    x = to_dev(inp["x"])
+    whole = M.MoELayer(cfg, wd).forward(x)["out"]
+    ranks = run_emulated(wl, [0, 77, 190], wd, x)
+    for s in ranks:
+        assert M.moe_check_device_status(s["ws"])[0] == M.MOE_OK
+    assert torch.equal(torch.cat([s["out"]["out"] for s in ranks]), whole)
+
+
+def test_pipeline_on_4_bit_experts():
+    T, d, ffn, E, k = 16, 64, 128, 4, 2
+    cfg = M.MoEConfig(T=T, d=d, ffn=ffn, E=E, k=k, capacity_factor=0.0, weights="int4_g128")
+    w = {"w_router": rand((d, E), 0.3, torch.bfloat16, 1), "w_gate": rand((E, d, ffn), 0.1, torch.bfloat16, 2),
+         "w_up": rand((E, d, ffn), 0.1, torch.bfloat16, 3), "w_down": rand((E, ffn, d), 0.1, torch.bfloat16, 4)}
+    wd = M.quantize_expert_weights(cfg, {n: v.cuda() for n, v in w.items()})
+    layer = M.MoELayer(cfg, wd)
+    with M.Pipeline(cfg, wd) as pipe:
+        xs = [rand((T, d), 1.0, torch.bfloat16, 10 + i).pin_memory() for i in range(3)]
+        outs = [torch.empty((T, d), dtype=torch.bfloat16).pin_memory() for _ in xs]
+        aux = [torch.empty(1).pin_memory() for _ in xs]
+        for x, o, a in zip(xs, outs, aux):
+            pipe.submit(x, o, a)
+        pipe.wait()
+        pipe.check()
+    for x, o in zip(xs, outs):
+        assert torch.equal(layer.forward(x.cuda())["out"].cpu(), o)
+
+
+@pytest.mark.parametrize("rows", [1, 15, 16, 17, 33, 64, 65, 129, 400])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_tile_borders(rows, group):
+    """One expert's rows around the tiles' borders, K and N around the blocks'; the same bits from one call of all
+    rows and from calls of each part of them."""
+    for K, N in ((120, 120), (128, 128), (136, 136), (256, 264), (392, 24)):
+        g, off, x, q, s, b, ws = case(([rows, 2], 0, K, N), group, seed=rows + K)
+        codes, sd, o = M.moe_pack_int4(q.cuda()), s.cuda(), torch.tensor(off, dtype=torch.int32).cuda()
+        y = torch.zeros((g.rows, N), dtype=torch.bfloat16, device="cuda")
+        xd = x.cuda()
+        M.moe_grouped_gemm_int4(g, xd, codes, sd, o, y, ws, group)
+        assert M.moe_check_device_status(ws)[0] == M.MOE_OK
+        for e in range(2):
+            xe, we = x[off[e]:off[e + 1]].double(), weight(q, s, group, e)
+            ref, mag = xe @ we, xe.abs() @ we.abs()
+            err = (y[off[e]:off[e + 1]].double().cpu() - ref).abs()
+            tol = (K / 8 + 64) * U * mag + HALF * ref.abs() + 1e-37
+            assert (err <= tol).all(), (K, N, float((err / tol).max()))
+        one = M.GroupedConfig(rows=1, E=2, K=K, N=N)
+        y1 = torch.zeros((1, N), dtype=torch.bfloat16, device="cuda")
+        M.moe_grouped_gemm_int4(one, xd[rows - 1:rows].contiguous(), codes, sd, torch.tensor([0, 1, 1], dtype=torch.int32).cuda(),
+                                y1, ws, group)
+        assert torch.equal(y1[0], y[rows - 1])
+
+
+def test_many_units_and_empty_experts():
+    """Long streams over many tiles per CTA, with experts that hold no row between others: the rings' parities."""
+    for group in (32, 64, 128):
+        for counts, K, N in (([0, 3] * 32, 2176, 1160), ([70, 0, 130], 2304, 2048)):
+            g, off, x, q, s, b, ws = case((counts, 0, K, N), group, seed=3)
+            y = torch.zeros((g.rows, N), dtype=torch.bfloat16, device="cuda")
+            xd, qd, sd = x.cuda(), q.cuda(), s.cuda()
+            for _ in range(3):
+                M.moe_grouped_gemm_int4(g, xd, M.moe_pack_int4(qd), sd, torch.tensor(off, dtype=torch.int32).cuda(), y, ws,
+                                        group)
+            assert M.moe_check_device_status(ws)[0] == M.MOE_OK
+            for e in range(g.E):
+                if off[e] == off[e + 1]:
+                    continue
+                we = (qd[e].double() * torch.repeat_interleave(sd[e].double(), group, dim=0)[:K])
+                xe = xd[off[e]:off[e + 1]].double()
+                ref, mag = xe @ we, xe.abs() @ we.abs()
+                err = (y[off[e]:off[e + 1]].double() - ref).abs()
+                assert (err <= (K / 8 + 64) * U * mag + HALF * ref.abs() + 1e-37).all()
