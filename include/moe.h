@@ -1,6 +1,7 @@
 /*
  * moe.h -- C ABI of libmoe, the forward pass of a top-k routed
- * Mixture-of-Experts FFN layer on NVIDIA B200 (sm_100a).
+ * Mixture-of-Experts FFN layer on NVIDIA B200 (sm_100a), and the expert
+ * products' gradients and 4-bit weights for training and serving it.
  *
  * The layer (pages that define it, by title and section):
  *   router        score = x . W_r, a bias-free linear router, then a softmax
@@ -333,7 +334,9 @@ moe_status_t moe_expert_ffn(const moe_config_t* cfg, const moe_weights_t* weight
  * [E+1] int32) are checked on the device: an expert whose offsets decrease or
  * leave [0, rows] is taken as empty and MOE_ERR_RANGE recorded.
  * Limits: 1 <= E <= 64; 0 <= rows < 2^31 - 1024.  The workspace holds
- * moe_grouped_workspace_size bytes (moe_workspace_init once). */
+ * moe_grouped_workspace_size bytes (moe_workspace_init once): the status block
+ * and, for gradients of few output tiles over many rows, the fp32 sums of the
+ * parts that an expert's rows are taken in, joined in a fixed order. */
 typedef struct {
     int64_t rows;   /* rows of the row buffers (offsets[E] at most) */
     int32_t E;      /* experts */

@@ -7,7 +7,10 @@ library is missing or fails to load, the calls raise.
 
 The functions below carry the C names (``moe_forward``, ``moe_router_topk``,
 ...) and take torch tensors (or None for optional pointers); ``MoELayer``
-bundles weights, outputs and workspace for the common case.
+bundles weights, outputs and workspace for the common case.  Training and
+serving use the same names: ``moe_grouped_gemm`` and its gradients on a
+``GroupedConfig``, ``moe_expert_ffn_backward``, and 4-bit experts through
+``MoEConfig(weights="int4_g64")`` with ``quantize_expert_weights``.
 """
 from __future__ import annotations
 
