@@ -32,6 +32,11 @@
 //              activation, bias and the store.
 // TN = 16 for batches of few rows per expert, 64 (SwiGLU, or groups of 32: 32)
 // for more: the host chooses by the mean.  Every wait is bounded in time, as in the other kernels.
+//
+// Measured: 128 rows over 64 experts of 2048 x 2048, groups of 64, 36 to 39 us, where the codes and scales take 20 at
+// the memory's rate (without the widening 32: the rest is the hand-over and 7 rounds of tiles for 6.2); 500 rows over
+// 8 experts of 4096 x 4096, groups of 128, 47 to 52 us (12): tiles of 64 tokens wait for the scaling warps (43
+// without), and an expert of more than 64 rows reads its codes again.
 #include <math.h>
 
 #include "gemm_common.cuh"
@@ -68,7 +73,7 @@ struct I4Smem {
     static constexpr int kStage = kScaleOff + kMats * kScales;
     // What is handed on at a time: kUnit blocks of 128 k of one matrix, its widened codes (64 columns a block) in one
     // of kABufs buffers in TMEM and its groups' accumulators (TN columns each) in one of kDBufs.  Handing on 256 k
-    // at TN = 16 halves the issuer's waits and commits, about 450 clocks a unit beside 36 for each MMA.
+    // at TN = 16 halves the issuer's waits and commits (64 experts of 2048 x 2048, 128 rows: 60 -> 38 us).
     static constexpr int kUnit = TN == 16 ? 2 : 1;
     static constexpr int kPerStage = 2 / kUnit * kMats;  // units of a stage: by half, then by matrix
     static constexpr int kACols = kUnit * 64, kDCols = kUnit * (4 / GS) * TN;
