@@ -370,7 +370,7 @@ moe_status_t moe_grouped_gemm_grad_w(const moe_grouped_config_t* cfg, const void
  * scale: float32 [E, ceil(K/group), N].
  *   moe_quantize_int4  from w [E, K, N] (the config's dtype): scale = max over
  *     the group |w| / 7, q = rint(w / scale) in fp32, ties to even (all-zero
- *     groups: scale 0, codes 0).
+ *     groups: scale 0, codes 0; groups with an infinity or NaN: scale NaN, codes 0).
  *   moe_pack_int4      from codes q [E, K, N] int8 (clamped to [-8, 7]) that come
  *     with scales of their own.
  * K <= 2^22, E * N < 2^31.  The config's rows do not matter to these two. */

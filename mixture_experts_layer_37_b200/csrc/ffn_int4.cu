@@ -499,8 +499,13 @@ __global__ void __launch_bounds__(128) quantize4_kernel(const void* __restrict__
         if (k0 >= K) break;
         if (!PACK && (32 * i) % group == 0) {
             float amax = 0.f;
-            for (int k = k0; k < min(k0 + group, K); ++k) amax = fmaxf(amax, fabsf(load(k)));
-            s = amax / 7.0f;
+            bool finite = true;
+            for (int k = k0; k < min(k0 + group, K); ++k) {
+                const float a = fabsf(load(k));
+                finite = finite && a < INFINITY;  // false for NaN, which fmaxf drops
+                amax = fmaxf(amax, a);
+            }
+            s = finite ? amax / 7.0f : NAN;  // no code stands for infinity or NaN: the products show it
             scale[(e * groups + k0 / group) * N + n] = s;
         }
 #pragma unroll

@@ -76,6 +76,33 @@ def test_quantise_codes_and_scales_exact(dtype, group):
     assert np.array_equal(codes.cpu().numpy(), pack_plain(want_q))
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_quantise_shows_values_without_a_code(bad, group):
+    """A group that holds an infinity or NaN gets the scale NaN and codes 0; the other groups keep theirs, and the
+    product is NaN in that expert's column alone."""
+    E, K, N, k, n = 2, 328, 72, 130, 5
+    w = rand((E, K, N), 0.02, torch.bfloat16, 6)
+    codes, scale = (t.cpu() for t in M.moe_quantize_int4(w.cuda(), group))
+    w[1, k, n] = bad
+    c2, s2 = M.moe_quantize_int4(w.cuda(), group)
+    want = scale.clone()
+    want[1, k // group, n] = float("nan")
+    assert torch.equal(torch.isnan(s2.cpu()), torch.isnan(want))
+    assert torch.equal(s2.cpu().nan_to_num(7.0), want.nan_to_num(7.0))
+    others = torch.ones(E, N, dtype=torch.bool)
+    others[1, n] = False
+    assert torch.equal(c2.cpu()[others], codes[others])
+    g = M.GroupedConfig(rows=6, E=E, K=K, N=N)
+    ws = M.Workspace(None, nbytes=M.moe_grouped_workspace_size(g))
+    y = torch.empty(6, N, device="cuda", dtype=torch.bfloat16)
+    M.moe_grouped_gemm_int4(g, rand((6, K), 1.0, torch.bfloat16, 7).cuda(), c2, s2,
+                            torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda"), y, ws, group)
+    expect = torch.zeros(6, N, dtype=torch.bool)
+    expect[2:, n] = True
+    assert torch.equal(torch.isnan(y.cpu()), expect)
+
+
 # counts per expert, rows behind the last one, K, N
 SHAPES = [
     ([1], 0, 8, 8),
