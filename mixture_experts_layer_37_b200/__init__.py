@@ -677,6 +677,8 @@ class GroupedConfig:
     dtype: str = "bf16"        # "bf16" | "f32"
 
     def __post_init__(self):
+        if self.dtype not in ("bf16", "f32"):
+            raise MoEError(MOE_ERR_INVALID_ARG, f"GroupedConfig: dtype {self.dtype!r}")
         # what every call needs, made once: a small call's time is mostly the host's
         object.__setattr__(self, "torch_dtype", torch.bfloat16 if self.dtype == "bf16" else torch.float32)
         object.__setattr__(self, "_c", MoEGroupedConfigC(self.rows, self.E, self.K, self.N,
@@ -690,6 +692,9 @@ class GroupedConfig:
 
     def c(self) -> MoEGroupedConfigC:
         return self._c
+
+    def __reduce__(self):  # the C struct is made anew: pointers are not copied
+        return GroupedConfig, (self.rows, self.E, self.K, self.N, self.dtype)
 
 
 _GCFG = ctypes.POINTER(MoEGroupedConfigC)
@@ -721,6 +726,13 @@ def _given(where: str, index: int, device, t, want) -> int:
     if t.shape != shape or t.dtype not in dtypes or t.get_device() != index or not t.is_contiguous():
         _refuse(where, t, shape, dtypes, device)
     return t.data_ptr()
+
+
+def _ws_on(where: str, index: int, ws: Workspace) -> tuple:
+    """The address and size of a workspace on CUDA device `index`."""
+    if ws.tensor.get_device() != index:
+        raise MoEError(MOE_ERR_INVALID_ARG, f"{where}: a workspace on cuda:{index} is wanted, got {ws.tensor.device}")
+    return ws.ptr, ws.nbytes
 
 
 def _expect(where: str, device, *specs) -> None:
@@ -768,7 +780,7 @@ def moe_grouped_gemm(g: GroupedConfig, x, w, offsets, y, ws: Workspace, bias=Non
     name, dev = "moe_grouped_gemm", w.device
     i = _cuda_index(name, dev)
     args = (g._ref, _given(name, i, dev, x, g._x), _given(name, i, dev, w, g._w), _given(name, i, dev, bias, g._b),
-            _given(name, i, dev, offsets, g._o), _given(name, i, dev, y, g._y), ws.ptr, ws.nbytes)
+            _given(name, i, dev, offsets, g._o), _given(name, i, dev, y, g._y), *_ws_on(name, i, ws))
     f = _fn("moe_grouped_gemm", _GCFG, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P)
     _call_on(dev, name, f, args, stream)
 
@@ -778,7 +790,7 @@ def moe_grouped_gemm_grad_x(g: GroupedConfig, dy, w, offsets, dx, ws: Workspace,
     name, dev = "moe_grouped_gemm_grad_x", w.device
     i = _cuda_index(name, dev)
     args = (g._ref, _given(name, i, dev, dy, g._y), _given(name, i, dev, w, g._w), _given(name, i, dev, offsets, g._o),
-            _given(name, i, dev, dx, g._x), ws.ptr, ws.nbytes)
+            _given(name, i, dev, dx, g._x), *_ws_on(name, i, ws))
     f = _fn("moe_grouped_gemm_grad_x", _GCFG, _P, _P, _P, _P, _P, ctypes.c_size_t, _P)
     _call_on(dev, name, f, args, stream)
 
@@ -791,7 +803,7 @@ def moe_grouped_gemm_grad_w(g: GroupedConfig, x, dy, offsets, dw, ws: Workspace,
     i = _cuda_index(name, dev)
     args = (g._ref, _given(name, i, dev, x, g._x), _given(name, i, dev, dy, g._y), _given(name, i, dev, offsets, g._o),
             _given(name, i, dev, dw, g._dw), _given(name, i, dev, db, (g._b[0], (dw.dtype,))), _dtype_code(dw.dtype),
-            1 if accumulate else 0, ws.ptr, ws.nbytes)
+            1 if accumulate else 0, *_ws_on(name, i, ws))
     f = _fn("moe_grouped_gemm_grad_w", _GCFG, _P, _P, _P, _P, _P, ctypes.c_int32, ctypes.c_int32, _P, ctypes.c_size_t,
             _P)
     _call_on(dev, name, f, args, stream)
@@ -830,7 +842,7 @@ def moe_expert_ffn_backward(cfg: MoEConfig, weights: dict, x_perm, offsets, dy_p
             ctypes.c_size_t, _P)
     _call_on(dev, "moe_expert_ffn_backward", f,
              (ctypes.byref(cfg.c()), ctypes.byref(wc), _ptr(x_perm), _ptr(offsets), _ptr(dy_perm), ctypes.byref(gc),
-              ws.ptr, ws.nbytes), stream)
+              *_ws_on("moe_expert_ffn_backward", dev.index, ws)), stream)
 
 
 # ---------------------------------------------------------------- 4-bit weights
@@ -873,6 +885,6 @@ def moe_grouped_gemm_int4(g: GroupedConfig, x, codes, scale, offsets, y, ws: Wor
     cs, ss = _int4_shapes(g.E, g.K, g.N, max(int(group), 1))
     args = (g._ref, _given(name, i, dev, x, g._x), _given(name, i, dev, codes, (cs, (torch.uint8,))),
             _given(name, i, dev, scale, (ss, (torch.float32,))), int(group), _given(name, i, dev, bias, g._b),
-            _given(name, i, dev, offsets, g._o), _given(name, i, dev, y, g._y), ws.ptr, ws.nbytes)
+            _given(name, i, dev, offsets, g._o), _given(name, i, dev, y, g._y), *_ws_on(name, i, ws))
     f = _fn("moe_grouped_gemm_int4", _GCFG, _P, _P, _P, ctypes.c_int32, _P, _P, _P, _P, ctypes.c_size_t, _P)
     _call_on(dev, name, f, args, stream)

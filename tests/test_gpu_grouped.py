@@ -550,3 +550,23 @@ def test_long_sums_in_fp32():
     M.moe_grouped_gemm_grad_w(g, x, dy, torch.tensor([0, g.rows], dtype=torch.int32).cuda(), dw, ws)
     ref = x.double().t() @ dy.double()
     assert float((dw[0].double() - ref).norm() / ref.norm()) <= 1e-6
+
+
+def test_a_workspace_of_another_device_is_refused():
+    g = M.GroupedConfig(rows=4, E=2, K=64, N=64)
+    d = dict(device="cuda", dtype=torch.bfloat16)
+    x, w, y = torch.zeros(4, 64, **d), torch.zeros(2, 64, 64, **d), torch.full((4, 64), 3.0, **d)
+    o = torch.tensor([0, 2, 4], device="cuda", dtype=torch.int32)
+    host = torch.empty(1 << 20, dtype=torch.uint8)
+    ws = type("W", (), {"tensor": host, "ptr": 1 << 20, "nbytes": host.numel()})()
+    codes, scale = M.moe_quantize_int4(w, 64)
+    cfg = M.MoEConfig(T=4, d=64, ffn=64, E=2, k=1)
+    sw = {"w_gate": w, "w_up": w, "w_down": w}
+    rows = torch.zeros(M.moe_max_rows(cfg), 64, **d)
+    for f in (lambda: M.moe_grouped_gemm(g, x, w, o, y, ws), lambda: M.moe_grouped_gemm_grad_x(g, x, w, o, y, ws),
+              lambda: M.moe_grouped_gemm_grad_w(g, x, x, o, w, ws),
+              lambda: M.moe_grouped_gemm_int4(g, x, codes, scale, o, y, ws, 64),
+              lambda: M.moe_expert_ffn_backward(cfg, sw, rows, o, rows, {"dx": torch.empty_like(rows)}, ws)):
+        with pytest.raises(M.MoEError, match="workspace"):
+            f()
+    assert torch.equal(y, torch.full_like(y, 3.0))

@@ -3,7 +3,10 @@ pass, on the host before any launch: no GPU is needed (pointers are never
 dereferenced)."""
 from __future__ import annotations
 
+import copy
 import ctypes
+import dataclasses
+import pickle
 
 import pytest
 import torch
@@ -180,6 +183,17 @@ def test_python_checks_tensors():
     with pytest.raises(M.MoEError):
         M.moe_expert_ffn_backward(M.MoEConfig(T=4, d=64, ffn=64, E=2, k=1), {}, z(4, 64), z(3, dtype=torch.int32), z(4, 64),
                                   {"w1": z(2, 64, 64)}, ws)   # a GELU name for SwiGLU experts
+
+
+def test_config_copies_and_types():
+    c = M.GroupedConfig(4, 2, 64, 128, "f32")
+    for d in (copy.copy(c), copy.deepcopy(c), pickle.loads(pickle.dumps(c)), dataclasses.replace(c)):
+        assert d == c and hash(d) == hash(c) and d is not c
+        assert (d.c().rows, d.c().E, d.c().K, d.c().N, d.c().dtype) == (4, 2, 64, 128, M.MOE_DT_F32)
+    assert dataclasses.replace(c, rows=9).c().rows == 9
+    for dtype in ("fp16", "float32", None):
+        with pytest.raises(M.MoEError):
+            M.GroupedConfig(4, 2, 64, 128, dtype)
 
 
 def test_struct_layouts_match_the_header():
