@@ -81,11 +81,12 @@ enum { FORM_FWD = 0, FORM_GX = 1, FORM_GW = 2 };
 // FWD, the backward pass of the expert activation (below).
 enum { EPI_BF16 = 0, EPI_F32 = 1, EPI_SWIGLU_GRAD = 2, EPI_GELU_GRAD = 3 };
 
-// fp32 outputs take twice the stores of a bf16 tile: two staging slabs per warp, one stage less.
-template <int FORM, int EPI>
+// fp32 outputs take twice the stores of a bf16 tile: two staging slabs per warp, one stage less (fp32 GW that adds to
+// 8 x 2048 x 4096 gradients, 8192 rows, measured together: 170 us; three slabs, four stages 177; four, three 193).
+template <int EPI>
 struct Smem {
-    static constexpr int kSlabs = EPI != EPI_F32 ? 1 : FORM == FORM_GW ? 2 : 2;
-    static constexpr int kStages = EPI != EPI_F32 ? 6 : FORM == FORM_GW ? 5 : 5;
+    static constexpr int kSlabs = EPI != EPI_F32 ? 1 : 2;
+    static constexpr int kStages = EPI != EPI_F32 ? 6 : 5;
     static constexpr int kSlabOff = kStages * kStageBytes;
     static constexpr int kBarOff = kSlabOff + kEpiWarps * kSlabs * kSlabBytes;
     static constexpr int kBytes = kBarOff + 512 + 1024 /*alignment*/;
@@ -291,7 +292,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmA2, const __grid_constant__ CUtensorMap tmB2,
                    const __grid_constant__ CUtensorMap tmO, GroupedParams p) {
-    using S = Smem<FORM, EPI>;
+    using S = Smem<EPI>;
     constexpr int kStages = S::kStages;
     constexpr bool kTwoB = EPI == EPI_SWIGLU_GRAD;  // gate and up halves of each CTA's columns
     constexpr bool kGw = FORM == FORM_GW;
@@ -700,6 +701,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
                 for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i >> 4][i & 15]);
             };
             if (kGrad) {
+                // N is a multiple of 32 here (bf16 layers have ffn % 64 == 0): every step of 32 columns is whole.
                 // dh comes in and h, the gradients go out through the slab, 32 columns at a time and 8 of them in
                 // registers.  Kept in loops: unrolled over a tile's columns, the activations came to more code than
                 // the instruction caches hold (GELU backward of 259 tokens, six launches: 82 us, in loops 73).
@@ -850,12 +852,12 @@ cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap
     int pairs_cap = dev < 64 ? max_pairs[dev].load(std::memory_order_acquire) : 0;
     if (pairs_cap <= 0) {
         cudaError_t err = cudaFuncSetAttribute(grouped_kernel<FORM, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               Smem<FORM, EPI>::kBytes);
+                                               Smem<EPI>::kBytes);
         if (err != cudaSuccess) return err;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * (unsigned)(sm_count() / 2));
         cfg.blockDim = dim3(kThreadsG);
-        cfg.dynamicSmemBytes = Smem<FORM, EPI>::kBytes;
+        cfg.dynamicSmemBytes = Smem<EPI>::kBytes;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
         attr.val.clusterDim.x = 2;
@@ -871,7 +873,7 @@ cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap
     }
     const int pairs = (int)min64(tiles_upper, (int64_t)pairs_cap);
     if (pairs <= 0) return cudaSuccess;
-    return launch_kernel(grouped_kernel<FORM, EPI>, dim3(2 * pairs), dim3(kThreadsG), Smem<FORM, EPI>::kBytes, s, a, b, a2, b2,
+    return launch_kernel(grouped_kernel<FORM, EPI>, dim3(2 * pairs), dim3(kThreadsG), Smem<EPI>::kBytes, s, a, b, a2, b2,
                          o, p);
 }
 
@@ -895,6 +897,7 @@ int64_t row_tiles_upper(const GroupedArgs& a) { return a.rows / BM + a.E; }
 
 cudaError_t launch_grouped_fwd_bf16(const GroupedArgs& a, cudaStream_t s) {
     CUtensorMap mA, mB, mB2, mO;
+    if (a.grad_act != GRAD_NONE && a.N % 32 != 0) return cudaErrorInvalidValue;  // its epilogue stores 32 columns whole
     const bool two = a.grad_act == GRAD_SWIGLU;
     bool ok = act_map(&mA, a.x, a.rows, a.K, 128);
     ok = ok && make_map_3d(&mB, a.w, a.E, a.K, a.N, false, 64, BK);
