@@ -28,15 +28,15 @@
 //              per stage, across tiles without a pause;
 //   warp 1     issues tcgen05.mma (A in TMEM, M=128, N=TN, K=16);
 //   then two or three groups of four warps that widen, taking units (I4Smem) in turn;
-//   last four warps that scale and add each group's sums, and at the tile's end
-//              activation, bias and the store.
+//   last four warps (eight from 32 tokens on) that scale and add each group's
+//              sums, and at the tile's end activation, bias and the store.
 // TN = 16 for batches of few rows per expert, 64 (SwiGLU, or groups of 32: 32)
 // for more: the host chooses by the mean.  Every wait is bounded in time, as in the other kernels.
 //
 // Measured: 128 rows over 64 experts of 2048 x 2048, groups of 64, 36 to 39 us, where the codes and scales take 20 at
 // the memory's rate (without the widening 32: the rest is the hand-over and 7 rounds of tiles for 6.2); 500 rows over
-// 8 experts of 4096 x 4096, groups of 128, 47 to 52 us (12): tiles of 64 tokens wait for the scaling warps (43
-// without), and an expert of more than 64 rows reads its codes again.
+// 8 experts of 4096 x 4096, groups of 128, 45 us (12): an expert of more than 64 rows takes its codes again.  (Tiles of
+// 128 tokens, which fit tensor memory for groups of 128 but leave two stages: 54 us, and slower at all sizes tried.)
 #include <math.h>
 
 #include "gemm_common.cuh"
@@ -50,7 +50,6 @@ using namespace gemm;
 constexpr int kBlockK = 128;                  // codes of a storage block
 constexpr int kCols = 128;                    // output columns of a tile
 constexpr int kCodeStage = kCols * 128;       // 16 KB: two blocks of each column
-constexpr int kScaleWarps = 4;
 
 enum { I4_PLAIN = 0, I4_SWIGLU = 1, I4_GELU = 2 };
 
@@ -87,6 +86,11 @@ struct I4Smem {
     // for tell that use from the one before.
     static_assert(kABufs % kGroupsOfWarps == 0, "each buffer belongs to one group of warps");
     static constexpr int kWidenWarps = 4 * kGroupsOfWarps;
+    // Four for each kTokens of the tile's tokens.  Four for all 64 (500 rows, 8 experts of 4096 x 4096: 47 us against
+    // 45; 1024 rows of 2048 x 2048, groups of 64: 32 against 27; SwiGLU FFN of 512 tokens, 16 experts of 2048 x 2048:
+    // 118 against 98) held the products up.  Four groups of widening warps instead of two: 46, 29 and 99 us.
+    static constexpr int kScaleWarps = TN == 16 ? 4 : 8;
+    static constexpr int kTokens = TN / (kScaleWarps / 4);
     static constexpr int kThreads = 32 * (2 + kWidenWarps + kScaleWarps);
     static constexpr int kStages = 200 * 1024 / kStage < 8 ? 200 * 1024 / kStage : 8;
     static constexpr int kBytes = kStages * kStage + 512 + 1024 /*alignment*/;
@@ -181,13 +185,13 @@ __global__ void __launch_bounds__(I4Smem<MODE, GS, TN>::kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], kScaleWarps);  // the last readers: they wait for the products
+            mbar_init(&empty[s], S::kScaleWarps);  // the last readers: they wait for the products
         }
         for (int b = 0; b < kABufs; ++b) {
             mbar_init(&ready[b], 4);
             mbar_init(&done[b], 1);
         }
-        for (int b = 0; b < kDBufs; ++b) mbar_init(&taken[b], kScaleWarps);
+        for (int b = 0; b < kDBufs; ++b) mbar_init(&taken[b], S::kScaleWarps);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -345,6 +349,8 @@ __global__ void __launch_bounds__(I4Smem<MODE, GS, TN>::kThreads, 1)
     } else {
         // ---------------------------------------------------- scales, sums and the store
         const int q = warp & 3;
+        constexpr int kTok = S::kTokens;
+        const int tok0 = ((warp - 2 - S::kWidenWarps) >> 2) * kTok;
         Ring<kStages> sb;
         Ring<kABufs> ab;
         Ring<kDBufs> db;
@@ -354,11 +360,11 @@ __global__ void __launch_bounds__(I4Smem<MODE, GS, TN>::kThreads, 1)
             if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
             const I4Tile t = i4_tile(tile, p, &tab, TN, place);
             const int n = t.n0 + 32 * q + lane;
-            float acc[kMats][TN];
+            float acc[kMats][kTok];
 #pragma unroll
             for (int m = 0; m < kMats; ++m)
 #pragma unroll
-                for (int j = 0; j < TN; ++j) acc[m][j] = 0.f;
+                for (int j = 0; j < kTok; ++j) acc[m][j] = 0.f;
 #pragma unroll 1
             for (int st = 0; st < nst && !stop; ++st, sb.next()) {
                 if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[sb.i], sb.par, tmo))) stop = true;
@@ -372,11 +378,11 @@ __global__ void __launch_bounds__(I4Smem<MODE, GS, TN>::kThreads, 1)
                     for (int g = 0; g < kG; ++g) sc[g] = scales[m * (S::kScales / 4) + (v / kMats * kGroups + g) * kCols];
                     if (!__all_sync(0xffffffffu, mbar_wait_bounded(&done[ab.i], ab.par, tmo))) stop = true;
                     tc_fence_after();
-                    const uint32_t src = d_base + ((uint32_t)(32 * q) << 16) + db.i * S::kDCols;
+                    const uint32_t src = d_base + ((uint32_t)(32 * q) << 16) + db.i * S::kDCols + tok0;
 #pragma unroll
                     for (int g = 0; g < kG; ++g)
 #pragma unroll
-                        for (int c = 0; c < TN; c += 16) {
+                        for (int c = 0; c < kTok; c += 16) {
                             uint32_t r[16];
                             tmem_ld_16(src + g * TN + c, r);
                             tmem_ld_wait();
@@ -397,10 +403,10 @@ __global__ void __launch_bounds__(I4Smem<MODE, GS, TN>::kThreads, 1)
             }
             if (n < p.N) {
                 const float bias = p.bias != nullptr ? __bfloat162float(p.bias[(int64_t)t.e * p.N + n]) : 0.f;
-                __nv_bfloat16* o = p.out + (int64_t)t.row0 * p.N + n;
+                __nv_bfloat16* o = p.out + (int64_t)(t.row0 + tok0) * p.N + n;
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    if (j < t.rows) {
+                for (int j = 0; j < kTok; ++j)
+                    if (tok0 + j < t.rows) {
                         float v = acc[0][j] + bias;
                         if (MODE == I4_SWIGLU) v = silu_f(v) * acc[kMats - 1][j];
                         if (MODE == I4_GELU) v = gelu_f(v);
@@ -446,11 +452,13 @@ cudaError_t launch_shape(const Int4Operands& o, Int4Params p, cudaStream_t s) {
 
 template <int MODE, int GS>
 cudaError_t launch_group(const Int4Operands& o, const Int4Params& p, cudaStream_t s) {
-    // Measured, tiles of 16 tokens against 64: 8 experts of 4096 x 4096, 16 rows each 29 against 32 us, 24 rows 37
-    // against 33; 64 experts of 2048 x 2048, 16 rows each 55 against 68 us, 24 rows 70 against 69.  Where 64 leave
-    // half the SMs without a tile, 16 are faster for any number of rows (2 of 1024 x 1024, 64 rows: 7.1 against 8.4).
+    // Measured, tiles of 16 tokens against 64: 8 experts of 4096 x 4096, 16 rows each 29.4 against 31.2 us, 20 rows
+    // 36.5 against 31.7; 64 experts of 2048 x 2048, 16 rows each 54.9 against 60.5 us, 20 rows 62.7 against 61.3 (groups
+    // of 32, against 32: 60.7 and 55.8, 70.2 and 56.3).  Where 64 leave two fifths of the SMs without a tile, 16 are
+    // faster for any number of rows (2 of 1024 x 1024, 64 rows: 7.1 against 7.9; 4 of 1024 x 2048, 24 rows: 6.9 against
+    // 8.4, but 32 rows, 96 tiles: 9.3 against 8.6).
     const int64_t tiles64 = ((int64_t)p.rows / 64 + p.E) * ((p.N + kCols - 1) / kCols);
-    if ((int64_t)p.rows <= 20 * (int64_t)p.E || 2 * tiles64 <= sm_count()) return launch_shape<MODE, GS, 16>(o, p, s);
+    if ((int64_t)p.rows <= 16 * (int64_t)p.E || 5 * tiles64 <= 3 * sm_count()) return launch_shape<MODE, GS, 16>(o, p, s);
     return launch_shape<MODE, GS, MODE == I4_SWIGLU || GS == 1 ? 32 : 64>(o, p, s);
 }
 

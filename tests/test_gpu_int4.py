@@ -351,3 +351,21 @@ def test_many_units_and_empty_experts():
                 ref, mag = xe @ we, xe.abs() @ we.abs()
                 err = (y[off[e]:off[e + 1]].double() - ref).abs()
                 assert (err <= (K / 8 + 64) * U * mag + HALF * ref.abs() + 1e-37).all()
+
+
+WIDE_ROWS = [31, 32, 33, 47, 48, 49, 63, 64, 65, 95, 97, 129]
+
+
+@pytest.mark.parametrize("rows", WIDE_ROWS)
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_wide_tile_borders(rows, group):
+    """Columns enough for the tiles of 32 and 64 tokens: rows around the borders of the tiles and of the tokens that
+    four of their warps take, a ragged last tile of columns, NaN rows behind."""
+    test_product(([rows, 2], 1, 200, 6152), group, True)
+
+
+@pytest.mark.parametrize("act", ["swiglu", "gelu_bias"])
+@pytest.mark.parametrize("rows", [31, 33, 48, 49, 64, 65])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_expert_ffn_wide_tile_borders(act, rows, group):
+    test_expert_ffn(act, group, [rows, 2], 64, 6144)
