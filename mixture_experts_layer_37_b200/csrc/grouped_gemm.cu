@@ -22,8 +22,11 @@
 // Measured alone the change gave 126 -> 121 us at 8192 x 2048 x 4096; elected
 // issuers then 115 -> 106 us, and 1525 -> 1366 us (1.61 PFLOP/s) at 65536 rows
 // of 4096 x 4096.  Now 105 us (1.31 PFLOP/s, of 83 us at the tensor cores'
-// peak); fp32 GW that adds to 268 MB of gradients, same sizes: 165 us, bound by
-// reading and writing them (98 us).
+// peak); tensor pipe busy 76 % of it; fp32 GW that adds to 268 MB of
+// gradients, same sizes: 165 us (98 us at the memory's rate, 139 without adding).
+// There neither memory (44 %) nor the tensor pipe (42 %) is full: a tile's sums
+// pass registers and slabs in turn.  Fetching the next tile's old values into L2
+// ahead changed nothing sure (169 -> 174 us, with uneven experts 170 -> 168).
 // What differs between the three forms is which operand is contiguous along
 // the contraction:
 //   FWD  A = x rows, contraction-major; B = W[e], output-major (two boxes
