@@ -71,16 +71,31 @@ class MoEOutputsC(ctypes.Structure):
                  "logits_out", "probs_out")]
 
 
-_lib = None
+_lib = None    # what callers of the C ABI get
+_bound = None  # what the functions below call
 _P = ctypes.c_void_p
 _CFG = ctypes.POINTER(MoEConfigC)
 
 
 def lib() -> ctypes.CDLL:
-    """Load libmoe.so (raises if it is missing: there is no fallback)."""
+    """Load libmoe.so (raises if it is missing: there is no fallback).  For calls of the C ABI;
+    the package calls through a handle of its own, so that argument types set here (or taken
+    away: ctypes then cuts addresses to 32 bits) do not change what its functions pass."""
     global _lib
-    if _lib is not None:
-        return _lib
+    if _lib is None:
+        _lib = _load()
+    return _lib
+
+
+def _own() -> ctypes.CDLL:
+    """The package's own handle on the library."""
+    global _bound
+    if _bound is None:
+        _bound = _load()
+    return _bound
+
+
+def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libmoe.so not built ({LIB_PATH}); run `python -m mixture_experts_layer_37_b200.build`")
     L = ctypes.CDLL(LIB_PATH)
@@ -112,7 +127,6 @@ def lib() -> ctypes.CDLL:
                  "moe_forward_hostio", "moe_check_device_status", "moe_selftest_bounded_wait",
                  "moe_forward_launch_count", "moe_forward_profiled"):
         getattr(L, name).restype = ctypes.c_int
-    _lib = L
     return L
 
 
@@ -188,24 +202,24 @@ def _check(status: int, where: str) -> None:
 
 
 def moe_status_string(status: int) -> str:
-    return lib().moe_status_string(status).decode()
+    return _own().moe_status_string(status).decode()
 
 
 def moe_capacity(cfg: MoEConfig) -> int:
     v = ctypes.c_int64()
-    _check(lib().moe_capacity(ctypes.byref(cfg.c()), ctypes.byref(v)), "moe_capacity")
+    _check(_own().moe_capacity(ctypes.byref(cfg.c()), ctypes.byref(v)), "moe_capacity")
     return v.value
 
 
 def moe_max_rows(cfg: MoEConfig) -> int:
     v = ctypes.c_int64()
-    _check(lib().moe_max_rows(ctypes.byref(cfg.c()), ctypes.byref(v)), "moe_max_rows")
+    _check(_own().moe_max_rows(ctypes.byref(cfg.c()), ctypes.byref(v)), "moe_max_rows")
     return v.value
 
 
 def moe_workspace_size(cfg: MoEConfig) -> int:
     v = ctypes.c_size_t()
-    _check(lib().moe_workspace_size(ctypes.byref(cfg.c()), ctypes.byref(v)), "moe_workspace_size")
+    _check(_own().moe_workspace_size(ctypes.byref(cfg.c()), ctypes.byref(v)), "moe_workspace_size")
     return v.value
 
 
@@ -218,23 +232,23 @@ class Workspace:
         off = (-self._buf.data_ptr()) % 1024
         self.tensor = self._buf[off:off + self.nbytes]
         self.ptr = self.tensor.data_ptr()
-        _check(lib().moe_workspace_init(self.ptr, self.nbytes, _stream(stream)), "moe_workspace_init")
+        _check(_own().moe_workspace_init(self.ptr, self.nbytes, _stream(stream)), "moe_workspace_init")
 
 
 def moe_workspace_init(ws: Workspace, stream=None) -> None:
-    _check(lib().moe_workspace_init(ws.ptr, ws.nbytes, _stream(stream)), "moe_workspace_init")
+    _check(_own().moe_workspace_init(ws.ptr, ws.nbytes, _stream(stream)), "moe_workspace_init")
 
 
 def moe_router_topk(cfg: MoEConfig, x, w_router, logit_bias, logits_in, topk_idx, topk_w, logits_out, probs_out,
                     ws: Workspace, stream=None, token_mask=None) -> None:
-    _check(lib().moe_router_topk(ctypes.byref(cfg.c()), _ptr(x), _ptr(w_router), _ptr(logit_bias), _ptr(logits_in),
+    _check(_own().moe_router_topk(ctypes.byref(cfg.c()), _ptr(x), _ptr(w_router), _ptr(logit_bias), _ptr(logits_in),
                                  _ptr(token_mask), _ptr(topk_idx), _ptr(topk_w), _ptr(logits_out), _ptr(probs_out),
                                  ws.ptr, ws.nbytes, _stream(stream)), "moe_router_topk")
 
 
 def moe_dispatch(cfg: MoEConfig, x, topk_idx, counts, offsets, slot, src_assign, x_perm, ws: Workspace,
                  stream=None) -> None:
-    _check(lib().moe_dispatch(ctypes.byref(cfg.c()), _ptr(x), _ptr(topk_idx), _ptr(counts), _ptr(offsets), _ptr(slot),
+    _check(_own().moe_dispatch(ctypes.byref(cfg.c()), _ptr(x), _ptr(topk_idx), _ptr(counts), _ptr(offsets), _ptr(slot),
                               _ptr(src_assign), _ptr(x_perm), ws.ptr, ws.nbytes, _stream(stream)), "moe_dispatch")
 
 
@@ -253,17 +267,17 @@ def _weights_c(w: dict) -> MoEWeightsC:
 
 def moe_expert_ffn(cfg: MoEConfig, weights: dict, x_perm, offsets, y_perm, ws: Workspace, stream=None) -> None:
     wc = _weights_c(weights)
-    _check(lib().moe_expert_ffn(ctypes.byref(cfg.c()), ctypes.byref(wc), _ptr(x_perm), _ptr(offsets), _ptr(y_perm),
+    _check(_own().moe_expert_ffn(ctypes.byref(cfg.c()), ctypes.byref(wc), _ptr(x_perm), _ptr(offsets), _ptr(y_perm),
                                 ws.ptr, ws.nbytes, _stream(stream)), "moe_expert_ffn")
 
 
 def moe_combine(cfg: MoEConfig, y_perm, slot, topk_w, out, stream=None) -> None:
-    _check(lib().moe_combine(ctypes.byref(cfg.c()), _ptr(y_perm), _ptr(slot), _ptr(topk_w), _ptr(out),
+    _check(_own().moe_combine(ctypes.byref(cfg.c()), _ptr(y_perm), _ptr(slot), _ptr(topk_w), _ptr(out),
                              _stream(stream)), "moe_combine")
 
 
 def moe_aux_stats(cfg: MoEConfig, counts, probs, f, p, l_aux, stream=None) -> None:
-    _check(lib().moe_aux_stats(ctypes.byref(cfg.c()), _ptr(counts), _ptr(probs), _ptr(f), _ptr(p), _ptr(l_aux),
+    _check(_own().moe_aux_stats(ctypes.byref(cfg.c()), _ptr(counts), _ptr(probs), _ptr(f), _ptr(p), _ptr(l_aux),
                                _stream(stream)), "moe_aux_stats")
 
 
@@ -300,7 +314,7 @@ def moe_forward(cfg: MoEConfig, weights: dict, x, outputs: dict, ws: Workspace, 
                 token_mask=None) -> None:
     wc = _weights_c(weights)
     oc = _outputs_c(outputs)
-    _check(lib().moe_forward(ctypes.byref(cfg.c()), ctypes.byref(wc), _ptr(x), _ptr(logits_in), _ptr(token_mask),
+    _check(_own().moe_forward(ctypes.byref(cfg.c()), ctypes.byref(wc), _ptr(x), _ptr(logits_in), _ptr(token_mask),
                              ctypes.byref(oc), ws.ptr, ws.nbytes, _stream(stream)), "moe_forward")
 
 
@@ -311,7 +325,7 @@ def moe_forward_profiled(cfg: MoEConfig, weights: dict, x, outputs: dict, ws: Wo
     wc = _weights_c(weights)
     oc = _outputs_c(outputs)
     arr = (ctypes.c_void_p * len(events))(*[ev.cuda_event for ev in events])
-    _check(lib().moe_forward_profiled(ctypes.byref(cfg.c()), ctypes.byref(wc), _ptr(x), _ptr(logits_in),
+    _check(_own().moe_forward_profiled(ctypes.byref(cfg.c()), ctypes.byref(wc), _ptr(x), _ptr(logits_in),
                                       _ptr(token_mask), ctypes.byref(oc), ws.ptr, ws.nbytes, _stream(stream), arr),
            "moe_forward_profiled")
 
@@ -320,7 +334,7 @@ def moe_forward_hostio(cfg: MoEConfig, weights: dict, x_host, x_dev, outputs: di
                        ws: Workspace, stream=None) -> None:
     wc = _weights_c(weights)
     oc = _outputs_c(outputs)
-    _check(lib().moe_forward_hostio(ctypes.byref(cfg.c()), ctypes.byref(wc), _ptr(x_host), _ptr(x_dev),
+    _check(_own().moe_forward_hostio(ctypes.byref(cfg.c()), ctypes.byref(wc), _ptr(x_host), _ptr(x_dev),
                                     ctypes.byref(oc), _ptr(out_host), _ptr(l_aux_host), ws.ptr, ws.nbytes,
                                     _stream(stream)), "moe_forward_hostio")
 
@@ -328,21 +342,21 @@ def moe_forward_hostio(cfg: MoEConfig, weights: dict, x_host, x_dev, outputs: di
 def moe_check_device_status(ws: Workspace, stream=None) -> tuple:
     """(status, site): synchronises the stream, reads and clears the status word."""
     site = ctypes.c_uint32(0)
-    st = lib().moe_check_device_status(ws.ptr, ws.nbytes, _stream(stream), ctypes.byref(site))
+    st = _own().moe_check_device_status(ws.ptr, ws.nbytes, _stream(stream), ctypes.byref(site))
     return st, site.value
 
 
 def moe_set_wait_timeout_ms(ms: int) -> None:
-    lib().moe_set_wait_timeout_ms(int(ms))
+    _own().moe_set_wait_timeout_ms(int(ms))
 
 
 def moe_selftest_bounded_wait(ws: Workspace, timeout_ms: int, stream=None) -> None:
-    _check(lib().moe_selftest_bounded_wait(ws.ptr, ws.nbytes, int(timeout_ms), _stream(stream)),
+    _check(_own().moe_selftest_bounded_wait(ws.ptr, ws.nbytes, int(timeout_ms), _stream(stream)),
            "moe_selftest_bounded_wait")
 
 
 def moe_forward_launch_count(cfg: MoEConfig) -> int:
-    return lib().moe_forward_launch_count(ctypes.byref(cfg.c()))
+    return _own().moe_forward_launch_count(ctypes.byref(cfg.c()))
 
 
 # ---------------------------------------------------------------- layer
@@ -391,7 +405,7 @@ def moe_dispatch_noalloc(cfg: MoEConfig, x, topk_idx, counts, offsets, slot, src
     """moe_dispatch without a workspace, for callers that cannot allocate device
     memory: the scratch lives in a fixed array inside the library (see
     include/moe.h for the size limit and the rule that calls must not overlap)."""
-    L = lib()
+    L = _own()
     f = L.moe_dispatch_noalloc
     f.argtypes = [_CFG, _P, _P, _P, _P, _P, _P, _P, _P]
     f.restype = ctypes.c_int
@@ -401,7 +415,7 @@ def moe_dispatch_noalloc(cfg: MoEConfig, x, topk_idx, counts, offsets, slot, src
 
 # ---------------------------------------------------------------- data-parallel shards of one batch
 def moe_dp_workspace_size(cfg: MoEConfig, T_global: int) -> int:
-    L = lib()
+    L = _own()
     f = L.moe_dp_workspace_size
     f.argtypes = [_CFG, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)]
     f.restype = ctypes.c_int
@@ -411,7 +425,7 @@ def moe_dp_workspace_size(cfg: MoEConfig, T_global: int) -> int:
 
 
 def moe_dp_max_rows(cfg: MoEConfig, T_global: int) -> int:
-    L = lib()
+    L = _own()
     f = L.moe_dp_max_rows
     f.argtypes = [_CFG, ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)]
     f.restype = ctypes.c_int
@@ -422,7 +436,7 @@ def moe_dp_max_rows(cfg: MoEConfig, T_global: int) -> int:
 
 def moe_dp_route(cfg: MoEConfig, T_global: int, weights: dict, x, outputs: dict, local_counts, local_psum,
                  ws: Workspace, logits_in=None, stream=None, token_mask=None, local_real=None) -> None:
-    L = lib()
+    L = _own()
     f = L.moe_dp_route
     f.argtypes = [_CFG, ctypes.c_int64, ctypes.POINTER(MoEWeightsC), _P, _P, _P, ctypes.POINTER(MoEOutputsC), _P, _P,
                   _P, _P, ctypes.c_size_t, _P]
@@ -436,7 +450,7 @@ def moe_dp_route(cfg: MoEConfig, T_global: int, weights: dict, x, outputs: dict,
 
 def moe_dp_finish(cfg: MoEConfig, T_global: int, all_counts, all_psum, world: int, rank: int, weights: dict, x,
                   outputs: dict, ws: Workspace, stream=None, all_real=None) -> None:
-    L = lib()
+    L = _own()
     f = L.moe_dp_finish
     f.argtypes = [_CFG, ctypes.c_int64, _P, _P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(MoEWeightsC), _P,
                   ctypes.POINTER(MoEOutputsC), _P, ctypes.c_size_t, _P]
@@ -472,7 +486,7 @@ def _ptr_array(ptrs) -> ctypes.Array:
 
 
 def _ep_fn(name: str, argtypes: list):
-    f = getattr(lib(), name)
+    f = getattr(_own(), name)
     f.argtypes = argtypes
     f.restype = ctypes.c_int
     return f
@@ -571,7 +585,7 @@ class Pipeline:
     untouched (inputs) or unread (outputs) until ``wait`` covers their step."""
 
     def __init__(self, cfg: MoEConfig, weights: dict, depth: int = 2):
-        L = lib()
+        L = _own()
         L.moe_pipeline_create.argtypes = [_CFG, ctypes.POINTER(MoEWeightsC), ctypes.c_int32, ctypes.POINTER(_P)]
         L.moe_pipeline_submit.argtypes = [_P, _P, _P, _P, _P, _P, ctypes.POINTER(ctypes.c_int64)]
         L.moe_pipeline_wait.argtypes = [_P, ctypes.c_int64]
@@ -629,7 +643,7 @@ def moe_quantize_int8(cfg: MoEConfig, w: torch.Tensor, stream=None):
     """INT8 codes and per-expert, per-output-column scales of expert weights
     w [E, K, N] (moe_quantize_int8).  Returns (codes int8 [E, K, N], scales
     float32 [E, N]), both on w's device."""
-    L = lib()
+    L = _own()
     f = L.moe_quantize_int8
     f.argtypes = [_CFG, _P, ctypes.c_int64, ctypes.c_int64, _P, _P, _P]
     f.restype = ctypes.c_int
@@ -705,7 +719,7 @@ def _fn(name: str, *argtypes):
     """The library's function `name`, declared once."""
     f = _fns.get(name)
     if f is None:
-        f = getattr(lib(), name)
+        f = getattr(_own(), name)
         f.argtypes = list(argtypes)
         f.restype = ctypes.c_int
         _fns[name] = f
