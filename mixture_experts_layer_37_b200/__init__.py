@@ -265,7 +265,37 @@ def _weights_c(w: dict) -> MoEWeightsC:
                        g("w_down_scale") if "w_down_scale" in w else g("w2_scale"))
 
 
+def _check_formats(where: str, cfg: MoEConfig, w: dict, E: Optional[int] = None) -> None:
+    """Refuses routed experts (E of them, the config's by default) stored in another form than
+    cfg.weights says.  The calls pass bare addresses, and the kernels take the tensors' extents
+    from the config: 4-bit scales of groups of 128 read as groups of 32 would be read four times
+    past their end, codes read as wider weights past theirs."""
+    first, down = "w_gate" if "w_gate" in w else "w1", "w_down" if "w_down" in w else "w2"  # as _weights_c picks them
+    if cfg.weights.startswith("int4"):
+        E, group, dev = cfg.E if E is None else E, WEIGHT_FORMATS[cfg.weights], None
+        for name, K, N in ((first, cfg.d, cfg.ffn), ("w_up", cfg.d, cfg.ffn), (down, cfg.ffn, cfg.d)):
+            if name == "w_up" and cfg.act != "swiglu":
+                continue
+            codes, scales = _int4_shapes(E, K, N, group)
+            for n, shape, dtype in ((name, codes, torch.uint8), (name + "_scale", scales, torch.float32)):
+                t = w.get(n)
+                if t is None:
+                    continue  # the library refuses a missing one
+                dev = t.device if dev is None else dev
+                if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+                    _refuse(f"{where}: {n} of {cfg.weights}", t, shape, dtype, dev)
+        if dev is not None:
+            _cuda_index(where, dev)
+        return
+    for n in (first, "w_up", down):
+        t = w.get(n)
+        if t is not None and (t.dtype == torch.uint8 or (t.dtype == torch.int8 and cfg.weights == "native")):
+            raise MoEError(MOE_ERR_INVALID_ARG, f"{where}: {n} holds codes ({t.dtype}), the config's weights are "
+                                                f"{cfg.weights!r}")
+
+
 def moe_expert_ffn(cfg: MoEConfig, weights: dict, x_perm, offsets, y_perm, ws: Workspace, stream=None) -> None:
+    _check_formats("moe_expert_ffn", cfg, weights)
     wc = _weights_c(weights)
     _check(_own().moe_expert_ffn(ctypes.byref(cfg.c()), ctypes.byref(wc), _ptr(x_perm), _ptr(offsets), _ptr(y_perm),
                                 ws.ptr, ws.nbytes, _stream(stream)), "moe_expert_ffn")
@@ -312,6 +342,7 @@ def allocate_outputs(cfg: MoEConfig, device="cuda", with_logits: bool = False, w
 
 def moe_forward(cfg: MoEConfig, weights: dict, x, outputs: dict, ws: Workspace, logits_in=None, stream=None,
                 token_mask=None) -> None:
+    _check_formats("moe_forward", cfg, weights)
     wc = _weights_c(weights)
     oc = _outputs_c(outputs)
     _check(_own().moe_forward(ctypes.byref(cfg.c()), ctypes.byref(wc), _ptr(x), _ptr(logits_in), _ptr(token_mask),
@@ -322,6 +353,7 @@ def moe_forward_profiled(cfg: MoEConfig, weights: dict, x, outputs: dict, ws: Wo
                          logits_in=None, stream=None, token_mask=None) -> None:
     """moe_forward recording torch.cuda.Event objects `events` (n+1 of them,
     n = moe_forward_launch_count) around each kernel launch on `stream`."""
+    _check_formats("moe_forward_profiled", cfg, weights)
     wc = _weights_c(weights)
     oc = _outputs_c(outputs)
     arr = (ctypes.c_void_p * len(events))(*[ev.cuda_event for ev in events])
@@ -332,6 +364,7 @@ def moe_forward_profiled(cfg: MoEConfig, weights: dict, x, outputs: dict, ws: Wo
 
 def moe_forward_hostio(cfg: MoEConfig, weights: dict, x_host, x_dev, outputs: dict, out_host, l_aux_host,
                        ws: Workspace, stream=None) -> None:
+    _check_formats("moe_forward_hostio", cfg, weights)
     wc = _weights_c(weights)
     oc = _outputs_c(outputs)
     _check(_own().moe_forward_hostio(ctypes.byref(cfg.c()), ctypes.byref(wc), _ptr(x_host), _ptr(x_dev),
@@ -364,6 +397,7 @@ class MoELayer:
     """Weights + preallocated outputs and workspace for repeated forwards."""
 
     def __init__(self, cfg: MoEConfig, weights: dict, device="cuda", with_logits=False, with_probs=False):
+        _check_formats("MoELayer", cfg, weights)
         self.cfg = cfg
         self.weights = weights
         self.outputs = allocate_outputs(cfg, device, with_logits, with_probs)
@@ -455,6 +489,7 @@ def moe_dp_finish(cfg: MoEConfig, T_global: int, all_counts, all_psum, world: in
     f.argtypes = [_CFG, ctypes.c_int64, _P, _P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(MoEWeightsC), _P,
                   ctypes.POINTER(MoEOutputsC), _P, ctypes.c_size_t, _P]
     f.restype = ctypes.c_int
+    _check_formats("moe_dp_finish", cfg, weights)
     wc = _weights_c(weights)
     oc = _outputs_c(outputs)
     _check(f(ctypes.byref(cfg.c()), int(T_global), _ptr(all_counts), _ptr(all_psum), _ptr(all_real), int(world),
@@ -535,6 +570,7 @@ def moe_ep_expert_ffn(cfg: MoEConfig, T_global: int, world: int, weights: dict, 
     """weights: this rank's experts (local_expert_weights) and the shared experts."""
     f = _ep_fn("moe_ep_expert_ffn", [_CFG, ctypes.c_int64, ctypes.c_int32, ctypes.POINTER(MoEWeightsC), _P, _P, _P,
                                      _P, _P, ctypes.c_size_t, _P])
+    _check_formats("moe_ep_expert_ffn", cfg, weights, cfg.E // max(int(world), 1))
     wc = _weights_c(weights)
     _check(f(ctypes.byref(cfg.c()), int(T_global), int(world), ctypes.byref(wc), _ptr(x), _ptr(x_recv),
              _ptr(recv_offsets), _ptr(y_recv), ws.ptr, ws.nbytes, _stream(stream)), "moe_ep_expert_ffn")
@@ -594,6 +630,7 @@ class Pipeline:
         for n in ("moe_pipeline_create", "moe_pipeline_submit", "moe_pipeline_wait", "moe_pipeline_check",
                   "moe_pipeline_destroy"):
             getattr(L, n).restype = ctypes.c_int
+        _check_formats("moe_pipeline_create", cfg, weights)
         self._L = L
         self.cfg = cfg
         self.weights = weights  # kept alive: the pipeline reads them on every step
