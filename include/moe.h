@@ -332,7 +332,8 @@ moe_status_t moe_expert_ffn(const moe_config_t* cfg, const moe_weights_t* weight
  * bf16: tensor cores, fp32 accumulation, one rounding of each output; K and N
  * multiples of 8.  f32: fp32 FMA; K and N multiples of 4.  offsets (DEVICE
  * [E+1] int32) are checked on the device: an expert whose offsets decrease or
- * leave [0, rows] is taken as empty and MOE_ERR_RANGE recorded.
+ * leave [0, rows], or that begins below the end of an expert before it, is taken
+ * as empty and MOE_ERR_RANGE recorded.
  * Limits: 1 <= E <= 64; 0 <= rows < 2^31 - 1024.  The workspace holds
  * moe_grouped_workspace_size bytes (moe_workspace_init once): the status block
  * and, for gradients of few output tiles over many rows, the fp32 sums of the

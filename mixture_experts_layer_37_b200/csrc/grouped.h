@@ -16,15 +16,37 @@ struct GroupTables {
 };
 
 #ifdef __CUDACC__
-// The rows of expert e.  Offsets that decrease or leave the buffers are
-// refused: such an expert has no rows, and the status word says so.
-__device__ __forceinline__ void group_rows(const int32_t* offsets, int rows, int e, const DevStatus& st, int& row0,
-                                           int& n) {
-    const int a = offsets[e], b = offsets[e + 1];
-    const bool ok = a >= 0 && b >= a && b <= rows;
-    if (!ok) report_range(st, SITE_GROUPED_OFFSETS);
-    row0 = ok ? a : 0;
-    n = ok ? b - a : 0;
+// The rows of experts lane and lane + 32, by a whole warp.  Offsets that decrease
+// or leave the buffers are refused: such an expert has no rows, and the status
+// word says so.  So has one that begins below the end of an expert before it
+// (possible only behind offsets that decrease): its rows are the other's, and two
+// tiles would write them.
+__device__ __forceinline__ void group_rows(const int32_t* offsets, int rows, int E, const DevStatus& st, int lane,
+                                           int (&row0)[2], int (&n)[2]) {
+    int carry = 0;  // the largest end so far
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int e = lane + 32 * i;
+        int a = 0, b = 0;
+        if (e < E) {
+            a = offsets[e];
+            b = offsets[e + 1];
+        }
+        const bool in = a >= 0 && b >= a && b <= rows;
+        int end = in ? b : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, end, d);
+            if (lane >= d) end = max(end, u);
+        }
+        int before = __shfl_up_sync(0xffffffffu, end, 1);
+        before = lane > 0 ? max(before, carry) : carry;
+        const bool ok = in && (a >= before || a == b);
+        if (e < E && !ok) report_range(st, SITE_GROUPED_OFFSETS);
+        row0[i] = ok ? a : 0;
+        n[i] = ok ? b - a : 0;
+        carry = max(carry, __shfl_sync(0xffffffffu, end, 31));
+    }
 }
 
 // The part z of S of expert e's rows (whole blocks of 64, the last parts may be empty).
@@ -41,13 +63,18 @@ __device__ __forceinline__ void part_rows(int S, int z, int& row0, int& n) {
 template <bool BY_ROWS>
 __device__ __forceinline__ void build_group_tables(const int32_t* offsets, int rows, int E, int bm, int m_tiles,
                                                    const DevStatus& st, GroupTables* t, int lane, int split = 1) {
-    int o[2] = {0, 0}, n[2] = {0, 0};
+    int o[2], n[2];
+    group_rows(offsets, rows, E / split, st, lane, o, n);
+    if (split > 1) {  // every expert's rows, then each part's own
+        const int oe[2] = {o[0], o[1]}, ne[2] = {n[0], n[1]};
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (lane + 32 * i < E) {
-            group_rows(offsets, rows, (lane + 32 * i) / split, st, o[i], n[i]);
-            if (split > 1) part_rows(split, (lane + 32 * i) % split, o[i], n[i]);
+        for (int i = 0; i < 2; ++i) {
+            const int e = (lane + 32 * i) / split;  // 32 experts at most are split
+            o[i] = __shfl_sync(0xffffffffu, oe[0], e & 31);
+            n[i] = __shfl_sync(0xffffffffu, ne[0], e & 31);
+            part_rows(split, (lane + 32 * i) % split, o[i], n[i]);
         }
+    }
     int rank[2] = {lane, lane + 32};
     if (BY_ROWS) {
         rank[0] = rank[1] = 0;

@@ -247,7 +247,7 @@ struct ColsumParams {
     ColsumJob job[2];
     int tiles0 = 0;  // tiles of 128 columns of the first job; the second's follow
     const int32_t* offsets = nullptr;
-    int rows = 0, accumulate = 0, split = 1;
+    int rows = 0, E = 0, accumulate = 0, split = 1;
     DevStatus st;
 };
 
@@ -273,8 +273,11 @@ __global__ void __launch_bounds__(kColWarps * 32) colsum_kernel(ColsumParams p) 
     const ColsumJob j = second ? p.job[1] : p.job[0];
     const int n0 = (blockIdx.x - (second ? p.tiles0 : 0)) * 128;
     const int e = blockIdx.y, col = n0 + lane * 4;
-    int row0, n;
-    group_rows(p.offsets, p.rows, e / p.split, p.st, row0, n);
+    int o[2], cnt[2];
+    group_rows(p.offsets, p.rows, p.E, p.st, lane, o, cnt);  // by every warp for itself
+    const int ex = e / p.split;
+    int row0 = __shfl_sync(0xffffffffu, ex < 32 ? o[0] : o[1], ex & 31);
+    int n = __shfl_sync(0xffffffffu, ex < 32 ? cnt[0] : cnt[1], ex & 31);
     if (p.split > 1) part_rows(p.split, e % p.split, row0, n);
     float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
     if (col < j.N)
@@ -418,6 +421,7 @@ cudaError_t launch_grouped_colsum(const GroupedArgs& a, const GroupedArgs* also,
     }
     p.offsets = a.offsets;
     p.rows = (int)a.rows;
+    p.E = a.E;
     p.accumulate = a.accumulate ? 1 : 0;
     p.split = a.split;
     p.st = a.st;

@@ -1,0 +1,103 @@
+"""Grouped products, their gradients and the FFN's backward pass where the arithmetic or the offsets are extreme,
+against float64.  Tolerances as in test_gpu_grouped: (n + 8) u A for fp32 chains, (n / 4 + 64) u A for the tensor
+cores' sums (u = 2^-24, A = the sum over the absolute values of the terms), half a step of the output's type."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import mixture_experts_layer_37_b200 as M
+from test_gpu_grouped import DT, HALF, U, check, rand
+from test_gpu_int4 import pack_plain, weight
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ offsets that give two experts the same rows
+OVERLAPS = [
+    [0, 900, 0, 900],                                  # the third expert has the first one's rows again
+    [0, 400, 200, 600, 600, 900],                      # and a part of them
+    [300, 310, 0, 305, 305, 900],                      # and all of them, from further ahead
+    [0, 500] + [500] * 36 + [100, 300, 900],           # an expert of the other half of the warp's lanes
+]
+
+
+def accepted(off, rows):
+    """[(first row, rows)] by the stated rule, one expert after the other."""
+    out, end = [], 0
+    for a, b in zip(off, off[1:]):
+        good = 0 <= a <= b <= rows
+        out.append((a, b - a) if good and (a >= end or a == b) else (0, 0))
+        end = max(end, b if good else 0)
+    return out
+
+
+@pytest.mark.parametrize("off", OVERLAPS, ids=lambda o: f"E{len(o) - 1}_{o[0]}_{o[2]}")
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_claimed_twice_belong_to_the_first(dtype, off):
+    E, rows, K, N, dt = len(off) - 1, 900, 72, 136, DT[dtype]
+    g = M.GroupedConfig(rows=rows, E=E, K=K, N=N, dtype=dtype)
+    ws = M.Workspace(None, nbytes=M.moe_grouped_workspace_size(g))
+    x, dy, w = rand((rows, K), 1.0, dt, 1), rand((rows, N), 0.1, dt, 2), rand((E, K, N), 0.05, dt, 3)
+    xd, dyd, wd, o = x.cuda(), dy.cuda(), w.cuda(), torch.tensor(off, dtype=torch.int32).cuda()
+    y = torch.full((rows, N), 5.0, dtype=dt, device="cuda")
+    dx = torch.full((rows, K), 5.0, dtype=dt, device="cuda")
+    dw, db = torch.full((E, K, N), 5.0, device="cuda"), torch.full((E, N), 5.0, device="cuda")
+    for f in (lambda: M.moe_grouped_gemm(g, xd, wd, o, y, ws), lambda: M.moe_grouped_gemm_grad_x(g, dyd, wd, o, dx, ws),
+              lambda: M.moe_grouped_gemm_grad_w(g, xd, dyd, o, dw, ws, db=db)):
+        f()
+        assert M.moe_check_device_status(ws) == (M.MOE_ERR_RANGE, 0x501)
+    written = torch.zeros(rows, dtype=torch.bool)
+    for e, (a, n) in enumerate(accepted(off, rows)):
+        assert not written[a:a + n].any()
+        written[a:a + n] = True
+        xe, de, we = x[a:a + n].double(), dy[a:a + n].double(), w[e].double()
+        check(y[a:a + n], xe @ we, xe.abs() @ we.abs(), K, dt)
+        check(dx[a:a + n], de @ we.t(), de.abs() @ we.abs().t(), N, dt)
+        check(dw[e], xe.t() @ de, xe.abs().t() @ de.abs(), n, dt)
+        check(db[e], de.sum(0), de.abs().sum(0), n, torch.float32)
+    assert (y.cpu()[~written] == 5.0).all() and (dx.cpu()[~written] == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_claimed_twice_with_rows_in_parts(dtype):
+    """The same where each expert's rows are summed in parts."""
+    rows, K, N, dt = 9000, 40, 64, DT[dtype]
+    off = [0, 9000, 2000, 9000]
+    g = M.GroupedConfig(rows=rows, E=3, K=K, N=N, dtype=dtype)
+    n = M.moe_grouped_workspace_size(g)
+    assert n > 64 * 1024
+    ws = M.Workspace(None, nbytes=n)
+    x, dy = rand((rows, K), 1.0, dt, 1), rand((rows, N), 0.1, dt, 2)
+    dw, db = torch.empty((3, K, N), device="cuda"), torch.empty((3, N), device="cuda")
+    M.moe_grouped_gemm_grad_w(g, x.cuda(), dy.cuda(), torch.tensor(off, dtype=torch.int32).cuda(), dw, ws, db=db)
+    assert M.moe_check_device_status(ws) == (M.MOE_ERR_RANGE, 0x501)
+    x, dy = x.double(), dy.double()
+    check(dw[0], x.t() @ dy, x.abs().t() @ dy.abs(), rows, dt)
+    check(db[0], dy.sum(0), dy.abs().sum(0), rows, torch.float32)
+    assert (dw[1:] == 0).all() and (db[1:] == 0).all()
+
+
+@pytest.mark.parametrize("off", OVERLAPS, ids=lambda o: f"E{len(o) - 1}_{o[0]}_{o[2]}")
+def test_int4_rows_claimed_twice_belong_to_the_first(off):
+    E, rows, K, N, group = len(off) - 1, 900, 136, 72, 64
+    g = M.GroupedConfig(rows=rows, E=E, K=K, N=N)
+    ws = M.Workspace(None, nbytes=M.moe_grouped_workspace_size(g))
+    gen = torch.Generator().manual_seed(4)
+    q = torch.randint(-8, 8, (E, K, N), dtype=torch.int8, generator=gen)
+    s = torch.rand((E, -(-K // group), N), generator=gen) * 0.01 + 0.002
+    x = rand((rows, K), 1.0, torch.bfloat16, 5)
+    y = torch.full((rows, N), 5.0, dtype=torch.bfloat16, device="cuda")
+    codes = torch.from_numpy(pack_plain(q.numpy())).cuda()
+    M.moe_grouped_gemm_int4(g, x.cuda(), codes, s.cuda(), torch.tensor(off, dtype=torch.int32).cuda(), y, ws, group)
+    assert M.moe_check_device_status(ws) == (M.MOE_ERR_RANGE, 0x501)
+    written = torch.zeros(rows, dtype=torch.bool)
+    for e, (a, n) in enumerate(accepted(off, rows)):
+        written[a:a + n] = True
+        we, xe = weight(q, s, group, e), x[a:a + n].double()
+        ref, mag = xe @ we, xe.abs() @ we.abs()
+        tol = (K / 8 + 64) * U * mag + HALF[torch.bfloat16] * ref.abs() + 1e-37
+        assert ((y[a:a + n].double().cpu() - ref).abs() <= tol).all()
+    assert (y.cpu()[~written] == 5.0).all()
