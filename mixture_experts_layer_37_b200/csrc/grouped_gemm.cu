@@ -85,10 +85,11 @@ enum { FORM_FWD = 0, FORM_GX = 1, FORM_GW = 2 };
 enum { EPI_BF16 = 0, EPI_F32 = 1, EPI_SWIGLU_GRAD = 2, EPI_GELU_GRAD = 3 };
 
 // fp32 outputs take twice the stores of a bf16 tile: two staging slabs per warp, one stage less (fp32 GW that adds to
-// 8 x 2048 x 4096 gradients, 8192 rows, measured together: 170 us; three slabs, four stages 177; four, three 193).
+// 8 x 2048 x 4096 gradients, 8192 rows, measured together: 160 us; three slabs, four stages 187; four, three 208).
 template <int EPI>
 struct Smem {
     static constexpr int kSlabs = EPI != EPI_F32 ? 1 : 2;
+    static_assert(kSlabs <= 2, "an accumulating tile refills its slabs two at a time");
     static constexpr int kStages = EPI != EPI_F32 ? 6 : 5;
     static constexpr int kSlabOff = kStages * kStageBytes;
     static constexpr int kBarOff = kSlabOff + kEpiWarps * kSlabs * kSlabBytes;
@@ -598,39 +599,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
                 float x[128];
 #pragma unroll
                 for (int i = 0; i < 128; ++i) x[i] = 0.f;
-                if (p.accumulate && rn > 0 && t.rows > 0) {
-                    // accumulating: what is there, loaded while the products run, slab by slab
+                // Accumulating: what is there waits in the slabs and is added once, to the finished sums (sums begun
+                // from it would be rounded at its magnitude by every run: 67 units in the last place after 32).  The
+                // first slabs are loaded while the products run, the others when these are stored: 8192 x 2048 x
+                // 4096, 8 experts, 160 us (uneven) and 142 (even); sums begun from the old values, all of them loaded
+                // meanwhile, 167 and 160; added by the memory (TMA reduction) 187 and 192.
+                const bool add = p.accumulate && rn > 0 && t.rows > 0;
+                auto load_old = [&](int c) {  // columns c.. into their slab (one lane)
+                    const int s = c / 32 % S::kSlabs;
+                    if (c >= ncols || col0 + c >= p.N) return;
+                    mbar_arrive_expect_tx(&old[s], kSlabBytes);
+                    tma_load_3d(slabs + s * kSlabBytes, &tmO, &old[s], col0 + c, row, t.e);
+                };
+                if (add) {
                     if (lane == 0) {
                         tma_store_wait_read<0>();
 #pragma unroll
-                        for (int s = 0; s < S::kSlabs; ++s)
-                            if (32 * s < ncols && col0 + 32 * s < p.N) {
-                                mbar_arrive_expect_tx(&old[s], kSlabBytes);
-                                tma_load_3d(slabs + s * kSlabBytes, &tmO, &old[s], col0 + 32 * s, row, t.e);
-                            }
+                        for (int s = 0; s < S::kSlabs; ++s) load_old(32 * s);
                     }
                     __syncwarp();
-                    bool in = true;
-#pragma unroll
-                    for (int c = 0; c < 128; c += 32) {
-                        const int s = c / 32 % S::kSlabs;
-                        if (c >= ncols || col0 + c >= p.N || !in) break;
-                        in = __all_sync(0xffffffffu, mbar_wait_bounded(&old[s], (old_par >> s) & 1u, tmo));
-                        old_par ^= 1u << s;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(x + c + 4 * j) =
-                            *slab_piece(slabs + s * kSlabBytes, lane, j);
-                        __syncwarp();
-                        constexpr int kNext = 32 * S::kSlabs;
-                        if (lane == 0 && in && c + kNext < ncols && col0 + c + kNext < p.N) {
-                            mbar_arrive_expect_tx(&old[s], kSlabBytes);
-                            tma_load_3d(slabs + s * kSlabBytes, &tmO, &old[s], col0 + c + kNext, row, t.e);
-                        }
-                    }
-                    if (!in) {
-                        if (lane == 0) give_up(SITE_GROUPED_OLD);
-                        break;
-                    }
                 }
                 const int runs = (tile_kblocks<FORM>(p, t) * BK + kRunRows - 1) / kRunRows;
                 bool ok = true;
@@ -649,8 +636,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
                     }
                     release();
                 }
-                if (!ok) break;
+                if (!ok) {
+                    if (add)  // the loads in flight land before the CTA leaves
+                        for (int s = 0; s < S::kSlabs; ++s)
+                            if (32 * s < ncols && col0 + 32 * s < p.N) mbar_wait_bounded(&old[s], (old_par >> s) & 1u, tmo);
+                    break;
+                }
                 if (rn <= 0 || (runs == 0 && p.accumulate)) continue;
+                if (add) {
+                    bool in = true;
+#pragma unroll
+                    for (int c = 0; c < 128; c += 32) {
+                        if (c >= ncols || col0 + c >= p.N || !in) break;
+                        const int s = c / 32 % S::kSlabs;
+                        uint8_t* slab = slabs + s * kSlabBytes;
+                        in = __all_sync(0xffffffffu, mbar_wait_bounded(&old[s], (old_par >> s) & 1u, tmo));
+                        old_par ^= 1u << s;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            float4* v = reinterpret_cast<float4*>(slab_piece(slab, lane, j));
+                            const float4 o = *v;
+                            const float* a = x + c + 4 * j;
+                            *v = make_float4(o.x + a[0], o.y + a[1], o.z + a[2], o.w + a[3]);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0 && in) {
+                            tma_store<true>(&tmO, slab, col0 + c, row, t.e);
+                            if (s == S::kSlabs - 1) {
+                                // the next columns into the slabs, each once its store has read it
+                                tma_store_wait_read<1>();
+                                load_old(c + 32);
+                                tma_store_wait_read<0>();
+                                load_old(c + 64);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (!in) {
+                        if (lane == 0) give_up(SITE_GROUPED_OLD);
+                        break;
+                    }
+                    continue;
+                }
 #pragma unroll
                 for (int c = 0; c < 128; c += 32) {
                     if (c >= ncols || col0 + c >= p.N) break;
@@ -659,9 +687,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
                     for (int j = 0; j < 8; ++j) *slab_piece(slab, lane, j) = pack4_f32(x + c + 4 * j);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
-                        tma_store<true>(&tmO, slab, col0 + c, row, t.e);
-                    }
+                    if (lane == 0) tma_store<true>(&tmO, slab, col0 + c, row, t.e);
                 }
                 continue;
             }

@@ -101,3 +101,33 @@ def test_int4_rows_claimed_twice_belong_to_the_first(off):
         tol = (K / 8 + 64) * U * mag + HALF[torch.bfloat16] * ref.abs() + 1e-37
         assert ((y[a:a + n].double().cpu() - ref).abs() <= tol).all()
     assert (y.cpu()[~written] == 5.0).all()
+
+
+# ------------------------------------------------------------------ what is there is added once
+@pytest.mark.parametrize("counts,K,N", [
+    ([16384], 2048, 2048),                  # 32 runs of rows for each accumulator, whole tiles
+    ([5000, 0, 1, 3111], 1304, 1320),       # ragged tiles of rows and of columns, an expert without rows
+    ([700, 1500], 2048, 1064),
+    ([512, 513, 40], 1672, 1688),
+], ids=lambda v: str(v) if isinstance(v, list) else None)
+def test_accumulating_adds_the_finished_sum_once(counts, K, N):
+    """fp32 gradients of bf16 rows, not in parts: with `accumulate` exactly what is there plus the sum that the call
+    without it gives, in one rounding, however much larger what is there may be."""
+    off = [0]
+    for n in counts:
+        off.append(off[-1] + n)
+    g = M.GroupedConfig(rows=off[-1] + 3, E=len(counts), K=K, N=N)
+    nb = M.moe_grouped_workspace_size(g)
+    ws = M.Workspace(None, nbytes=nb)
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.randn((g.rows, K), generator=gen, device="cuda").bfloat16()
+    dy = torch.randn((g.rows, N), generator=gen, device="cuda").bfloat16()
+    o = torch.tensor(off, dtype=torch.int32).cuda()
+    total = torch.empty((g.E, K, N), device="cuda")
+    M.moe_grouped_gemm_grad_w(g, x, dy, o, total, ws)
+    for scale in (1e6, 1.0, 0.0):
+        old = torch.randn((g.E, K, N), generator=gen, device="cuda") * scale
+        dw = old.clone()
+        M.moe_grouped_gemm_grad_w(g, x, dy, o, dw, ws, accumulate=True)
+        assert M.moe_check_device_status(ws)[0] == M.MOE_OK
+        assert torch.equal(dw, old + total)
