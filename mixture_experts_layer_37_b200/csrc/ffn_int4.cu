@@ -409,7 +409,11 @@ __global__ void __launch_bounds__(I4Smem<MODE, GS, TN>::kThreads, 1)
                     if (tok0 + j < t.rows) {
                         float v = acc[0][j] + bias;
                         if (MODE == I4_SWIGLU) v = silu_f(v) * acc[kMats - 1][j];
-                        if (MODE == I4_GELU) v = gelu_f(v);
+                        if (MODE == I4_GELU) {
+                            float cdf, pdf;
+                            normal_cdf_pdf(v, cdf, pdf);
+                            v *= cdf;
+                        }
                         o[(int64_t)j * p.N] = __float2bfloat16_rn(v);
                     }
             }

@@ -16,6 +16,31 @@ struct GroupTables {
 };
 
 #ifdef __CUDACC__
+// The normal distribution Phi and its density phi, each to its own relative precision.  (1 + erf(x / sqrt 2)) / 2
+// cancels for negative x: at -5 it is off by a tenth, behind -5.5 it is noise or zero, and so are x Phi(x) and its
+// gradients.
+// fp32: by erfc.
+__device__ __forceinline__ float normal_cdf(float x) { return 0.5f * erfcf(x * -0.70710678118654752f); }
+// Where results are rounded to bf16: from phi, which the gradient needs anyway, and the Mills ratio
+// Phi(-z) / phi(z) = t P(t), t = 1 / (1 + 0.35 z), P a polynomial fitted here for the least relative error over
+// 0 <= z <= 14.6 (3.2e-8, evaluated in fp32 3.4e-7; phi has the fast exponential's error).  With erfc the GELU
+// backward pass of 8192 rows, 8 experts of 2048 x 4096, took 732 us where this takes 668, 777 rows of 192 x 320 59 for 51.
+__device__ __forceinline__ void normal_cdf_pdf(float x, float& cdf, float& pdf) {
+    pdf = 0.39894228040143268f * __expf(-0.5f * x * x);
+    const float t = __fdividef(1.0f, fmaf(0.35f, fabsf(x), 1.0f));
+    float q = -0.0730919167f;
+    q = fmaf(q, t, 0.3610515f);
+    q = fmaf(q, t, -0.641334414f);
+    q = fmaf(q, t, 0.399403274f);
+    q = fmaf(q, t, -0.0582185797f);
+    q = fmaf(q, t, 0.264595568f);
+    q = fmaf(q, t, 0.300343603f);
+    q = fmaf(q, t, 0.350586385f);
+    q = fmaf(q, t, 0.349978685f);
+    const float tail = pdf * (q * t);
+    cdf = x < 0.0f ? tail : 1.0f - tail;
+}
+
 // The rows of experts lane and lane + 32, by a whole warp.  Offsets that decrease
 // or leave the buffers are refused: such an expert has no rows, and the status
 // word says so.  So has one that begins below the end of an expert before it

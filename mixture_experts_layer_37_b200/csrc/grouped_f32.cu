@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(256) act_grad_f32_kernel(int64_t n, float* g, 
         g[i] = d * uv * (s + xs * (1.0f - s));
         u[i] = d * xs;
     } else {
-        const float cdf = 0.5f * (1.0f + erff(x * 0.70710678118654752f));
+        const float cdf = normal_cdf(x);
         dh[i] = x * cdf;
         g[i] = d * (cdf + x * 0.39894228040143268f * expf(-0.5f * x * x));
     }

@@ -285,8 +285,8 @@ __device__ __forceinline__ void swiglu_grad(float g, float u, float dh, float& h
     du = dh * gs;
 }
 __device__ __forceinline__ void gelu_grad(float p, float dh, float& h, float& dp) {
-    const float cdf = 0.5f * (1.0f + erff(p * 0.70710678118654752f));
-    const float pdf = 0.39894228040143268f * __expf(-0.5f * p * p);
+    float cdf, pdf;
+    normal_cdf_pdf(p, cdf, pdf);
     h = p * cdf;
     dp = dh * (cdf + p * pdf);
 }

@@ -131,3 +131,62 @@ def test_accumulating_adds_the_finished_sum_once(counts, K, N):
         M.moe_grouped_gemm_grad_w(g, x, dy, o, dw, ws, accumulate=True)
         assert M.moe_check_device_status(ws)[0] == M.MOE_OK
         assert torch.equal(dw, old + total)
+
+
+# ------------------------------------------------------------------ GELU far below zero
+def tail_case(ffn, dtype):
+    """Pre-activations from -9 to 1 (exact in bf16), and in float64 Phi, phi, h = p Phi(p) and h' = Phi + p phi of them."""
+    p = torch.linspace(-9, 1, ffn).to(dtype)
+    q = p.double()
+    cdf = 0.5 * torch.special.erfc(-q / math.sqrt(2))
+    pdf = torch.exp(-q * q / 2) / math.sqrt(2 * math.pi)
+    return p, q, cdf, pdf
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gelu_gradients_in_the_tail(dtype):
+    """h and dp where Phi is small keep their own relative precision: one token, one row of dy, so that each gradient
+    is a single term.  Phi from an argument rounded once has p^2 u (and 1.6 p^2 u for the scaled argument), its four
+    units in the last place 8 u; the exponential of p^2 / 2 as much (bf16: its fast form about 100 u more); the
+    products 3 u.  bf16 rounds h and dp to its type once."""
+    d, ffn, dt = 64, 128, DT[dtype]
+    cfg = M.MoEConfig(T=1, d=d, ffn=ffn, E=1, k=1, dtype=dtype, act="gelu_bias", capacity_factor=0.0)
+    p, q, cdf, pdf = tail_case(ffn, dt)
+    w1, w2 = torch.zeros(1, d, ffn, dtype=dt), rand((1, ffn, d), 1.0, dt, 3)
+    x, dy = torch.zeros(1, d, dtype=dt), torch.zeros(1, d, dtype=dt)
+    x[0, 5], dy[0, 9] = 1.5, 0.75
+    w = {"w1": w1, "b1": p[None], "w2": w2, "b2": torch.zeros(1, d, dtype=dt)}
+    grads = {n: torch.empty(v.shape, device="cuda") for n, v in w.items()}
+    ws = M.Workspace(None, nbytes=M.moe_expert_ffn_backward_workspace_size(cfg))
+    M.moe_expert_ffn_backward(cfg, {n: v.cuda() for n, v in w.items()}, x.cuda(),
+                              torch.tensor([0, 1], dtype=torch.int32).cuda(), dy.cuda(), grads, ws)
+    assert M.moe_check_device_status(ws)[0] == M.MOE_OK
+    step = 1.01 * HALF[dt] if dtype == "bf16" else 0.0
+    rel = (3 * q * q + 20 + (100 if dtype == "bf16" else 0)) * U
+    h, dh = q * cdf, 0.75 * w2[0, :, 9].double()
+    dp, dp_mag = dh * (cdf + q * pdf), dh.abs() * (cdf + (q * pdf).abs())
+    got = {n: v[0].double().cpu() for n, v in grads.items()}
+    for name, g, ref, mag in (("h", got["w2"][:, 9], 0.75 * h, (0.75 * h).abs()), ("dp", got["b1"], dp, dp_mag),
+                              ("dw1", got["w1"][5], 1.5 * dp, 1.5 * dp_mag)):
+        err, tol = (g - ref).abs(), rel * mag + step * ref.abs()
+        assert (err <= tol).all(), (name, float((err / tol).max()))
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_int4_gelu_in_the_tail(group):
+    """The 4-bit FFN's h likewise: codes of 0 before the activation, an identity behind it."""
+    d = ffn = 128
+    cfg = M.MoEConfig(T=2, d=d, ffn=ffn, E=1, k=1, act="gelu_bias", capacity_factor=0.0, weights=f"int4_g{group}")
+    p, q, cdf, _ = tail_case(ffn, torch.bfloat16)
+    eye = torch.eye(ffn, dtype=torch.int8)[None].cuda()
+    ones = torch.ones(1, -(-d // group), ffn, device="cuda")
+    w = {"w1": M.moe_pack_int4(torch.zeros_like(eye)), "w1_scale": ones, "b1": p[None].cuda(),
+         "w2": M.moe_pack_int4(eye), "w2_scale": ones, "b2": torch.zeros(1, d, dtype=torch.bfloat16, device="cuda")}
+    ws, y = M.Workspace(cfg), torch.empty(2, d, dtype=torch.bfloat16, device="cuda")
+    M.moe_expert_ffn(cfg, w, rand((2, d), 1.0, torch.bfloat16, 1).cuda(), torch.tensor([0, 2], dtype=torch.int32).cuda(), y, ws)
+    assert M.moe_check_device_status(ws)[0] == M.MOE_OK
+    h = q * cdf
+    tol = ((3 * q * q + 20) * U + 1.01 * HALF[torch.bfloat16]) * h.abs()
+    for r in (0, 1):
+        err = (y[r].double().cpu() - h).abs()
+        assert (err <= tol).all(), float((err / tol).max())
