@@ -676,6 +676,29 @@ class Pipeline:
             pass
 
 
+class _FromCurrent:
+    """For calls that make their outputs: a tensor belongs to the stream that is current when it is made, so work on
+    another `stream` begins behind the current one (whose earlier work may still use the memory) and the current one
+    goes on behind it (where the outputs are then read, or freed).  Yields the stream to launch on."""
+
+    def __init__(self, device, stream):
+        raw = None if stream is None else _stream(stream)
+        self.current = torch.cuda.current_stream(device)
+        self.on = self.current
+        if raw is not None and raw != self.current.cuda_stream:
+            self.on = stream if isinstance(stream, torch.cuda.Stream) else \
+                torch.cuda.default_stream(device) if raw == 0 else torch.cuda.ExternalStream(raw, device)
+
+    def __enter__(self):
+        if self.on is not self.current:
+            self.on.wait_stream(self.current)
+        return self.on
+
+    def __exit__(self, *exc):
+        if self.on is not self.current:
+            self.current.wait_stream(self.on)
+
+
 def moe_quantize_int8(cfg: MoEConfig, w: torch.Tensor, stream=None):
     """INT8 codes and per-expert, per-output-column scales of expert weights
     w [E, K, N] (moe_quantize_int8).  Returns (codes int8 [E, K, N], scales
@@ -687,7 +710,8 @@ def moe_quantize_int8(cfg: MoEConfig, w: torch.Tensor, stream=None):
     E, K, N = w.shape
     q = torch.empty((E, K, N), dtype=torch.int8, device=w.device)
     s = torch.empty((E, N), dtype=torch.float32, device=w.device)
-    _check(f(ctypes.byref(cfg.c()), _ptr(w), int(K), int(N), _ptr(q), _ptr(s), _stream(stream)), "moe_quantize_int8")
+    with _FromCurrent(w.device, stream) as on:
+        _check(f(ctypes.byref(cfg.c()), _ptr(w), int(K), int(N), _ptr(q), _ptr(s), _stream(on)), "moe_quantize_int8")
     return q, s
 
 
@@ -911,8 +935,8 @@ def moe_quantize_int4(w: torch.Tensor, group: int, stream=None) -> tuple:
     codes = torch.empty(cs, dtype=torch.uint8, device=w.device)
     scale = torch.empty(ss, dtype=torch.float32, device=w.device)
     f = _fn("moe_quantize_int4", _GCFG, _P, ctypes.c_int32, _P, _P, _P)
-    _call_on(w.device, "moe_quantize_int4", f, (g._ref, _ptr(w), int(group), _ptr(codes), _ptr(scale)),
-             stream)
+    with _FromCurrent(w.device, stream) as on:
+        _call_on(w.device, "moe_quantize_int4", f, (g._ref, _ptr(w), int(group), _ptr(codes), _ptr(scale)), on)
     return codes, scale
 
 
@@ -924,7 +948,8 @@ def moe_pack_int4(q: torch.Tensor, stream=None) -> torch.Tensor:
     _expect("moe_pack_int4", q.device, (q, (E, K, N), (torch.int8,)))
     codes = torch.empty(_int4_shapes(E, K, N, 128)[0], dtype=torch.uint8, device=q.device)
     f = _fn("moe_pack_int4", _GCFG, _P, _P, _P)
-    _call_on(q.device, "moe_pack_int4", f, (g._ref, _ptr(q), _ptr(codes)), stream)
+    with _FromCurrent(q.device, stream) as on:
+        _call_on(q.device, "moe_pack_int4", f, (g._ref, _ptr(q), _ptr(codes)), on)
     return codes
 
 
