@@ -36,7 +36,8 @@
 // Measured: 128 rows over 64 experts of 2048 x 2048, groups of 64, 36 to 39 us, where the codes and scales take 20 at
 // the memory's rate (without the widening 32: the rest is the hand-over and 7 rounds of tiles for 6.2); 500 rows over
 // 8 experts of 4096 x 4096, groups of 128, 45 us (12): an expert of more than 64 rows takes its codes again.  (Tiles of
-// 128 tokens, which fit tensor memory for groups of 128 but leave two stages: 54 us, and slower at all sizes tried.)
+// 128 tokens fit tensor memory for groups of 128 but leave two stages, fewer than the waits below need; 54 us was
+// measured so, which settles nothing.)
 #include <math.h>
 
 #include "gemm_common.cuh"
@@ -93,6 +94,10 @@ struct I4Smem {
     static constexpr int kTokens = TN / (kScaleWarps / 4);
     static constexpr int kThreads = 32 * (2 + kWidenWarps + kScaleWarps);
     static constexpr int kStages = 200 * 1024 / kStage < 8 ? 200 * 1024 / kStage : 8;
+    // A widening group skips the stages that hold none of its units and waits for `full` by parity. Before it waits for
+    // unit u it has seen the products of unit u - kGroupsOfWarps - kABufs done, so their stage and all before it were
+    // full; if that one lies less than kStages behind, the fill before the awaited one is over and cannot be taken for it.
+    static_assert(kStages * kPerStage >= kGroupsOfWarps + kABufs, "stages enough to wait for a fill by its parity");
     static constexpr int kBytes = kStages * kStage + 512 + 1024 /*alignment*/;
 };
 
