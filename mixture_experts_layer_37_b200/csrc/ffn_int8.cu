@@ -90,21 +90,6 @@ struct QArgs {
 __device__ __forceinline__ float silu_q(float x) { return x / (1.0f + __expf(-x)); }
 __device__ __forceinline__ float gelu_q(float x) { return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f)); }
 
-// Packed pairs of fp32 values (the f32x2 arithmetic of sm_100: two independent
-// fp32 operations per instruction, each rounded as its scalar form).
-__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));

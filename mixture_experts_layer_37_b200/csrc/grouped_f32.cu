@@ -34,35 +34,20 @@ struct F32Params {
     DevStatus st;
 };
 
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
 // One operand's [TK x T] piece: PER float4 per thread, from memory that is
 // contiguous along the tile (KC = false) or along the contraction (KC = true).
 // base points at tile element 0, contraction element 0; ld is the stride of
 // the other axis; t_n, k_n say how many of each exist from here.
 template <int T, int TK, bool KC>
 struct Piece {
-    static constexpr int PER = T * TK / 4 / kF32Threads > 0 ? T * TK / 4 / kF32Threads : 1;
-    static constexpr bool kAll = T * TK / 4 >= kF32Threads;
+    static constexpr int PER = T * TK / 4 / kF32Threads;
+    static_assert(PER * 4 * kF32Threads == T * TK, "whole pieces");
     float4 v[PER];
     __device__ __forceinline__ void load(const float* base, int64_t ld, int t_n, int k0, int k_n) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int id = threadIdx.x + i * kF32Threads;
             v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (!kAll && id >= T * TK / 4) continue;
             const int k = k0 + (KC ? id % (TK / 4) * 4 : id / (T / 4));
             const int t = KC ? id / (TK / 4) : id % (T / 4) * 4;
             if (k < k_n && t < t_n)
@@ -73,7 +58,6 @@ struct Piece {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int id = threadIdx.x + i * kF32Threads;
-            if (!kAll && id >= T * TK / 4) continue;
             if (KC) {
                 const int k = id % (TK / 4) * 4, t = id / (TK / 4);
                 s[k][t] = v[i].x;
@@ -217,7 +201,8 @@ cudaError_t launch_form(const GroupedArgs& a, const F32Params& p, int out_m, int
     // 64 x 128 (256 tiles), 146 us with 64 x 64, 200 us with 128 x 128 (128); GW 101 us with 128 x 128 (512 tiles),
     // 107 us with 64 x 128; 512 x 512, 512 rows, FWD 24 us with 64 x 64 (64 tiles), 35 us with 64 x 128, 30 us with
     // 32 x 32; 128 x 256, 4 experts, 128 rows, 4.9 us with 32 x 32, 7.4 us with 64 x 64 (8 tiles).
-    if (FORM == FORM_GW && tiles(128, 128) >= 2 * sms) return launch_tiles<FORM, 128, 128, 16>(p, out_m, out_n, s);
+    if constexpr (FORM == FORM_GW)
+        if (tiles(128, 128) >= 2 * sms) return launch_tiles<FORM, 128, 128, 16>(p, out_m, out_n, s);
     if (tiles(64, 128) >= sms) return launch_tiles<FORM, 64, 128, 16>(p, out_m, out_n, s);
     if (tiles(64, 64) >= sms / 3) return launch_tiles<FORM, 64, 64, 32>(p, out_m, out_n, s);
     return launch_tiles<FORM, 32, 32, 32>(p, out_m, out_n, s);
