@@ -70,8 +70,17 @@ def parse():
     ap.add_argument("--dispatch", default="auto", choices=["auto", "copy", "gather"])
     ap.add_argument("--n-shared", type=int, default=None, help="shared experts (default: the workload's)")
     ap.add_argument("--pad-fraction", type=float, default=None, help="padding tokens (default: the workload's)")
-    ap.add_argument("--weights", default=None, choices=["native", "int8"], help="routed experts' weight storage")
+    ap.add_argument("--weights", default=None, choices=["native", "int8", "int4_g32", "int4_g64", "int4_g128"],
+                    help="routed experts' weight storage")
     return ap.parse_args()
+
+
+def weight_bytes(fmt, native):
+    """Bytes per weight of the routed experts (native: those of the dtype): codes, and for the 4-bit forms the
+    fp32 scale of each group (INT8's, one per column, are left out)."""
+    if fmt.startswith("int4_g"):
+        return 0.5 + 4 / int(fmt[len("int4_g"):])
+    return 1 if fmt == "int8" else native
 
 
 def peaks():
@@ -261,7 +270,7 @@ def bench_workload(a, name: str, steps: int, warmup: int, cpu_seconds: float, wo
     weights = {n: dev(inp[n]) for n in wnames if n in inp}
     if inp.get("router_bias") is not None:
         weights["router_bias"] = dev(np.asarray(inp["router_bias"], dtype=np.float32))
-    if wl.weights == "int8":
+    if wl.weights != "native":
         weights = M.quantize_expert_weights(cfg, weights)  # once, before anything is timed
         torch.cuda.synchronize()
     x = dev(inp["x"])
@@ -349,7 +358,7 @@ def bench_workload(a, name: str, steps: int, warmup: int, cpu_seconds: float, wo
     # each expert GEMM is bound by the tensor cores or by streaming the weights of
     # the experts that received rows, whichever its FLOP per byte puts it under
     hit = int((layer.outputs["offsets"].diff() > 0).sum().item())
-    wbpe = 1 if wl.weights == "int8" else bpe
+    wbpe = weight_bytes(wl.weights, bpe)
     nmat1 = 2 if wl.act == "swiglu" else 1
     gemm1_bytes = hit * nmat1 * wl.d * wl.ffn * wbpe + R * (wl.d + wl.ffn) * bpe
     gemm2_bytes = hit * wl.d * wl.ffn * wbpe + R * (wl.d + wl.ffn) * bpe

@@ -107,7 +107,8 @@ class Workload:
     seed: int = 0
     n_shared: int = 0         # always-on shared experts (same FFN form as the routed ones)
     pad_fraction: float = 0.0  # expected fraction of padding tokens (token_mask = 0)
-    weights: str = "native"   # routed experts' weights: "native" (the dtype), "int8" or "int4_g64" etc. (quantised by the layer)
+    weights: str = "native"   # routed experts' weights: "native" (the dtype), or the form that they are quantised to before
+    #                           the layer gets them: "int8", "int4_g32", "int4_g64" or "int4_g128"
 
     def with_(self, **kw) -> "Workload":
         return replace(self, **kw)
