@@ -337,9 +337,13 @@ moe_status_t moe_expert_ffn(const moe_config_t* cfg, const moe_weights_t* weight
  * Limits: 1 <= E <= 64; 0 <= rows < 2^31 - 1024.  The workspace holds
  * moe_grouped_workspace_size bytes (moe_workspace_init once): the status block
  * and, for gradients of few output tiles over many rows, the fp32 sums of the
- * parts that an expert's rows are taken in, joined in a fixed order. */
+ * parts that an expert's rows are taken in, joined in a fixed order.
+ * Tiles and parts are planned on the host, which does not read the offsets, by
+ * `rows` and E: buffers much longer than offsets[E] get the plan of the longer
+ * batch (4-bit products: tiles for many rows per expert; weight gradients: the
+ * parts, whose order of sums moves the last bits). */
 typedef struct {
-    int64_t rows;   /* rows of the row buffers (offsets[E] at most) */
+    int64_t rows;   /* rows of the row buffers, offsets[E] or more */
     int32_t E;      /* experts */
     int32_t K;      /* columns of x: rows of each expert's matrix */
     int32_t N;      /* columns of y: columns of each expert's matrix */
@@ -401,7 +405,8 @@ typedef struct {
  * the forward pass: the inner activations are formed again from x_perm, in
  * fp32, inside the product that needs them, and rounded to the dtype once
  * where the next product reads them; the gradient of the inner activation is
- * kept in fp32.  dy_perm is the gradient of the unweighted expert outputs (a
+ * kept in fp32.  b1's gradient is the fp32 sum of its argument's gradients as
+ * rounded for the products: the values that W1's gradient sums.  dy_perm is the gradient of the unweighted expert outputs (a
  * weighted combine hands down topk_w[t,j] * dout[t]).  Native weights only;
  * shared experts are expert FFNs of one group and take a config of E = k = 1.
  * The workspace holds moe_expert_ffn_backward_workspace_size bytes. */

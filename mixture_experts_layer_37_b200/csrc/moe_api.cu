@@ -1395,7 +1395,9 @@ moe_status_t moe_expert_ffn_backward(const moe_config_t* cfg, const moe_weights_
     out.db = db2;
     if (grouped_gw(out, bf16, at(ws, pl.parts), stream) != cudaSuccess) return MOE_ERR_CUDA;
     in.x = x_perm;
-    in.dy = d0;
+    in.dy = d0;  // bf16: rounded for the products.  db1 sums these too, in fp32: each term is off by 2^-8 of itself at
+                 // most, as in dW1.  (Unrounded terms would take column sums in the activation's epilogue and one
+                 // more launch to join them.)
     in.dw = grads->w_gate_or_w1;
     in.db = db1;
     if (grouped_gw(in, bf16, at(ws, pl.parts), stream) != cudaSuccess) return MOE_ERR_CUDA;
