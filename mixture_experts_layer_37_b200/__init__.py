@@ -15,6 +15,7 @@ serving use the same names: ``moe_grouped_gemm`` and its gradients on a
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -265,33 +266,48 @@ def _weights_c(w: dict) -> MoEWeightsC:
                        g("w_down_scale") if "w_down_scale" in w else g("w2_scale"))
 
 
+@functools.lru_cache(maxsize=64)
+def _int4_specs(fmt: str, E: int, d: int, ffn: int, swiglu: bool) -> tuple:
+    """(name, its other act's name, shape, dtype) of each code and scale tensor of a 4-bit format."""
+    group, out = WEIGHT_FORMATS[fmt], []
+    for name, other, K, N in (("w_gate", "w1", d, ffn), ("w_up", "w_up", d, ffn), ("w_down", "w2", ffn, d)):
+        if name == "w_up" and not swiglu:
+            continue
+        codes, scales = _int4_shapes(E, K, N, group)
+        out.append((name, other, torch.Size(codes), torch.uint8))
+        out.append((name + "_scale", other + "_scale", torch.Size(scales), torch.float32))
+    return tuple(out)
+
+
+_CODES = {"native": (torch.uint8, torch.int8), "int8": (torch.uint8,)}  # types that hold less than the format's weights
+
+
 def _check_formats(where: str, cfg: MoEConfig, w: dict, E: Optional[int] = None) -> None:
     """Refuses routed experts (E of them, the config's by default) stored in another form than
     cfg.weights says.  The calls pass bare addresses, and the kernels take the tensors' extents
     from the config: 4-bit scales of groups of 128 read as groups of 32 would be read four times
     past their end, codes read as wider weights past theirs."""
-    first, down = "w_gate" if "w_gate" in w else "w1", "w_down" if "w_down" in w else "w2"  # as _weights_c picks them
-    if cfg.weights.startswith("int4"):
-        E, group, dev = cfg.E if E is None else E, WEIGHT_FORMATS[cfg.weights], None
-        for name, K, N in ((first, cfg.d, cfg.ffn), ("w_up", cfg.d, cfg.ffn), (down, cfg.ffn, cfg.d)):
-            if name == "w_up" and cfg.act != "swiglu":
-                continue
-            codes, scales = _int4_shapes(E, K, N, group)
-            for n, shape, dtype in ((name, codes, torch.uint8), (name + "_scale", scales, torch.float32)):
-                t = w.get(n)
-                if t is None:
-                    continue  # the library refuses a missing one
-                dev = t.device if dev is None else dev
-                if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
-                    _refuse(f"{where}: {n} of {cfg.weights}", t, shape, dtype, dev)
-        if dev is not None:
-            _cuda_index(where, dev)
+    codes = _CODES.get(cfg.weights)
+    if codes is not None:
+        for n in ("w_gate", "w1", "w_up", "w_down", "w2"):
+            t = w.get(n)
+            if t is not None and t.dtype in codes:
+                raise MoEError(MOE_ERR_INVALID_ARG, f"{where}: {n} holds codes ({t.dtype}), the config's weights are "
+                                                    f"{cfg.weights!r}")
         return
-    for n in (first, "w_up", down):
+    device = None
+    for name, other, shape, dtype in _int4_specs(cfg.weights, cfg.E if E is None else E, cfg.d, cfg.ffn,
+                                                 cfg.act == "swiglu"):
+        n = name if name in w else other  # as _weights_c picks them
         t = w.get(n)
-        if t is not None and (t.dtype == torch.uint8 or (t.dtype == torch.int8 and cfg.weights == "native")):
-            raise MoEError(MOE_ERR_INVALID_ARG, f"{where}: {n} holds codes ({t.dtype}), the config's weights are "
-                                                f"{cfg.weights!r}")
+        if t is None:
+            continue  # the library refuses a missing one
+        if device is None:
+            device = t.device
+        if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+            _refuse(f"{where}: {n} of {cfg.weights}", t, shape, dtype, device)
+    if device is not None:
+        _cuda_index(where, device)
 
 
 def moe_expert_ffn(cfg: MoEConfig, weights: dict, x_perm, offsets, y_perm, ws: Workspace, stream=None) -> None:
