@@ -405,10 +405,10 @@ typedef struct {
  * the forward pass: the inner activations are formed again from x_perm, in
  * fp32, inside the product that needs them, and rounded to the dtype once
  * where the next product reads them; the gradient of the inner activation is
- * kept in fp32.  b1's gradient is the fp32 sum of its argument's gradients as
- * rounded for the products: the values that W1's gradient sums.  dy_perm is the gradient of the unweighted expert outputs (a
- * weighted combine hands down topk_w[t,j] * dout[t]).  Native weights only;
- * shared experts are expert FFNs of one group and take a config of E = k = 1.
+ * kept in fp32, and so is its argument's where b1's gradient sums it.  dy_perm
+ * is the gradient of the unweighted expert outputs (a weighted combine hands
+ * down topk_w[t,j] * dout[t]).  Native weights only; shared experts are expert
+ * FFNs of one group and take a config of E = k = 1.
  * The workspace holds moe_expert_ffn_backward_workspace_size bytes. */
 moe_status_t moe_expert_ffn_backward_workspace_size(const moe_config_t* cfg, size_t* bytes);
 moe_status_t moe_expert_ffn_backward(const moe_config_t* cfg, const moe_weights_t* weights, const void* x_perm,

@@ -81,6 +81,11 @@ __device__ __forceinline__ void part_rows(int S, int z, int& row0, int& n) {
     n = min(per, n - from);
 }
 
+// Column sums of 32 rows each ("slabs", counted from an expert's first row): where expert e's begin. Experts' rows do
+// not overlap and come in order, so their slabs do not either; rows / 32 + E of them at most.
+__host__ __device__ __forceinline__ int64_t max_slabs(int64_t rows, int E) { return rows / 32 + E; }
+__device__ __forceinline__ int first_slab(int row0, int e) { return (row0 >> 5) + e; }
+
 // One warp; each lane holds experts `lane` and `lane + 32`.  BY_ROWS: experts
 // in order of falling row count (ties: lower id) with m_tiles tiles each; else
 // in their own order with one tile per bm rows.  split > 1: E counts the parts
@@ -168,6 +173,9 @@ struct GroupedArgs {
     void* h = nullptr;                 // [rows, N] activation
     void* d0 = nullptr;                // [rows, N] gradient of gate (SwiGLU) or of the pre-activation (GELU)
     void* d1 = nullptr;                // [rows, N] gradient of up (SwiGLU)
+    // GELU: d0's column sums by slabs of 32 rows, [max_slabs, N] fp32, written by FWD with the activation's backward
+    // pass and read instead of dy by the bias gradient; or null
+    float* sums = nullptr;
     DevStatus st;
 };
 

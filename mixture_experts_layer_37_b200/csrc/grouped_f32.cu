@@ -224,9 +224,10 @@ F32Params params(const GroupedArgs& a) {
 constexpr int kColWarps = 16;  // a lane holds 4 columns
 
 struct ColsumJob {
-    const void* dy = nullptr;  // [rows, N]
+    const void* dy = nullptr;  // [rows, N], or fp32 sums of slabs of its rows
     void* db = nullptr;        // [E, N], or [E, split, N]
     int N = 0;
+    bool slabs = false;
 };
 struct ColsumParams {
     ColsumJob job[2];
@@ -248,6 +249,9 @@ __device__ __forceinline__ float4 load4(const void* base, int64_t i) {
 // One CTA per (expert or part of its rows, 128 columns): warp w adds the rows w,
 // w+16, ... in two interleaved sums, eight rows loaded at a time (the loads'
 // latency bounds this kernel), and the warps' sums are added in a fixed order.
+// b1's gradient of a bf16 GELU FFN takes, instead of rows, the sums of 32 rows
+// each that the activation's epilogue left (unrounded, where the rows themselves
+// are rounded for the products).
 template <bool IN_BF16, bool OUT_BF16>
 __global__ void __launch_bounds__(kColWarps * 32) colsum_kernel(ColsumParams p) {
     __shared__ float4 part[kColWarps][32];
@@ -263,15 +267,22 @@ __global__ void __launch_bounds__(kColWarps * 32) colsum_kernel(ColsumParams p) 
     const int ex = e / p.split;
     int row0 = __shfl_sync(0xffffffffu, ex < 32 ? o[0] : o[1], ex & 31);
     int n = __shfl_sync(0xffffffffu, ex < 32 ? cnt[0] : cnt[1], ex & 31);
+    const int first = row0;
     if (p.split > 1) part_rows(p.split, e % p.split, row0, n);
+    if (j.slabs) {  // parts are whole slabs
+        row0 = first_slab(first, ex) + ((row0 - first) >> 5);
+        n = (n + 31) >> 5;
+    }
     float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
     if (col < j.N)
         for (int r = warp; r < n; r += 8 * kColWarps) {
             float4 v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = r + kColWarps * i < n ? load4<IN_BF16>(j.dy, (int64_t)(row0 + r + kColWarps * i) * j.N + col)
-                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = 0; i < 8; ++i) {
+                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                const int64_t at = (int64_t)(row0 + r + kColWarps * i) * j.N + col;
+                if (r + kColWarps * i < n) v[i] = j.slabs ? load4<false>(j.dy, at) : load4<IN_BF16>(j.dy, at);
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 s[i & 1].x += v[i].x;
@@ -398,7 +409,8 @@ cudaError_t launch_grouped_colsum(const GroupedArgs& a, const GroupedArgs* also,
     int tiles = 0;
     for (int i = 0; i < (also != nullptr ? 2 : 1); ++i) {
         const GroupedArgs& g = i == 0 ? a : *also;
-        p.job[i].dy = g.dy;
+        p.job[i].dy = g.sums != nullptr ? g.sums : g.dy;
+        p.job[i].slabs = g.sums != nullptr;
         p.job[i].db = g.db;
         p.job[i].N = g.N;
         tiles += (g.N + 127) / 128;

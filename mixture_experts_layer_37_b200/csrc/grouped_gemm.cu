@@ -112,6 +112,7 @@ struct GroupedParams {
     __nv_bfloat16* h = nullptr;           // [rows, N] outputs
     __nv_bfloat16* d0 = nullptr;
     __nv_bfloat16* d1 = nullptr;
+    float* sums = nullptr;                // GELU: [slabs, N] column sums of d0 before its rounding, or null
     DevStatus st;
 };
 
@@ -289,6 +290,20 @@ __device__ __forceinline__ void gelu_grad(float p, float dh, float& h, float& dp
     normal_cdf_pdf(p, cdf, pdf);
     h = p * cdf;
     dp = dh * (cdf + p * pdf);
+}
+
+// The sums over a warp's lanes of eight values each, value lane / 4 in this lane: every step but the last two halves
+// the values that a lane keeps.
+__device__ __forceinline__ float sum_lanes_8(float (&v)[8], int lane) {
+#pragma unroll
+    for (int w = 16, n = 4; w >= 4; w >>= 1, n >>= 1)
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float give = lane & w ? v[i] : v[i + n], keep = lane & w ? v[i + n] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+        }
+    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
 template <int FORM, int EPI>
@@ -771,6 +786,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
                             bias[0] = bias[1];
                             bias[1] = bias[2];
                             bias[2] = bias[3];
+                            if (p.sums != nullptr) {  // b1's gradient: d0 summed as it is before its rounding
+                                float v[8];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) v[i] = lane < rn ? x[i] : 0.f;
+                                const float sum = sum_lanes_8(v, lane);
+                                const int64_t at = first_slab(t.row0 - t.m0, t.e) + ((t.m0 + r0) >> 5);
+                                if (rn > 0 && (lane & 3) == 0) p.sums[at * p.N + col + 8 * s + (lane >> 2)] = sum;
+                            }
                         } else {
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
@@ -950,6 +973,7 @@ cudaError_t launch_grouped_fwd_bf16(const GroupedArgs& a, cudaStream_t s) {
     p.h = static_cast<__nv_bfloat16*>(a.h);
     p.d0 = static_cast<__nv_bfloat16*>(a.d0);
     p.d1 = static_cast<__nv_bfloat16*>(a.d1);
+    p.sums = a.sums;
     const int64_t tiles = row_tiles_upper(a) * p.n_tiles;
     if (two) return launch<FORM_FWD, EPI_SWIGLU_GRAD>(mA, mB, mA, mB2, mO, p, tiles, s);
     if (a.grad_act == GRAD_GELU) return launch<FORM_FWD, EPI_GELU_GRAD>(mA, mB, mA, mB2, mO, p, tiles, s);

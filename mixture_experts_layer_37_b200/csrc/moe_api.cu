@@ -1153,7 +1153,7 @@ cudaError_t grouped_db(const GroupedArgs& a, const GroupedArgs* also, bool bf16,
 }
 
 struct BackwardPlan {
-    size_t dh, h, d0, d1, parts, total;
+    size_t dh, h, d0, d1, sums, parts, total;
 };
 BackwardPlan backward_plan(const moe_config_t* c) {
     const size_t n = (size_t)max_rows(c) * c->ffn, s = elem_size(c);
@@ -1167,6 +1167,9 @@ BackwardPlan backward_plan(const moe_config_t* c) {
     off = align_up(off + n * s, 1024);
     p.d1 = off;  // gradient of up
     off = align_up(off + (c->act == MOE_ACT_SWIGLU ? n * s : 0), 1024);
+    p.sums = off;  // bf16 GELU: column sums of d0 by slabs of 32 rows, before its rounding
+    if (c->dtype == MOE_DT_BF16 && c->act == MOE_ACT_GELU_BIAS)
+        off = align_up(off + (size_t)max_slabs(max_rows(c), c->E) * c->ffn * 4, 1024);
     p.parts = off;  // of the gradients of one [E, d, ffn] or [E, ffn, d], and of b1 and b2, one after the other
     const bool bf16 = c->dtype == MOE_DT_BF16;
     const int64_t rows = max_rows(c);
@@ -1369,6 +1372,7 @@ moe_status_t moe_expert_ffn_backward(const moe_config_t* cfg, const moe_weights_
     a.w = weights->w_gate_or_w1;
     a.bias = swiglu ? nullptr : weights->b1;
     if (bf16) {
+        a.sums = in.sums = db1 != nullptr ? reinterpret_cast<float*>(at(ws, pl.sums)) : nullptr;
         a.w2 = weights->w_up;
         a.grad_act = swiglu ? GRAD_SWIGLU : GRAD_GELU;
         a.dh = dh;
@@ -1395,9 +1399,7 @@ moe_status_t moe_expert_ffn_backward(const moe_config_t* cfg, const moe_weights_
     out.db = db2;
     if (grouped_gw(out, bf16, at(ws, pl.parts), stream) != cudaSuccess) return MOE_ERR_CUDA;
     in.x = x_perm;
-    in.dy = d0;  // bf16: rounded for the products.  db1 sums these too, in fp32: each term is off by 2^-8 of itself at
-                 // most, as in dW1.  (Unrounded terms would take column sums in the activation's epilogue and one
-                 // more launch to join them.)
+    in.dy = d0;
     in.dw = grads->w_gate_or_w1;
     in.db = db1;
     if (grouped_gw(in, bf16, at(ws, pl.parts), stream) != cudaSuccess) return MOE_ERR_CUDA;

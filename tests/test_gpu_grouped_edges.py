@@ -190,3 +190,68 @@ def test_int4_gelu_in_the_tail(group):
     for r in (0, 1):
         err = (y[r].double().cpu() - h).abs()
         assert (err <= tol).all(), float((err / tol).max())
+
+
+# ------------------------------------------------------------------ b1's gradient
+@pytest.mark.parametrize("counts,behind", [
+    ([1], 0), ([5], 3), ([31, 1, 33], 2), ([0, 64, 2, 0, 127, 128, 129], 9), ([300, 255, 257], 0), ([3] * 40, 1),
+    ([2100, 0, 3001], 5),                   # the experts' rows in parts
+], ids=lambda v: f"E{len(v)}_R{sum(v)}" if isinstance(v, list) else None)
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_b1_gradient_sums_unrounded_terms(counts, behind, accumulate):
+    """bf16 GELU: dp = dh gelu'(p) is rounded to bf16 for the products, but not where b1's gradient sums it.  With x = 0
+    p is b1, and with one column of dy dh is one product: a term is off by what test_gelu_gradients_in_the_tail states,
+    the fp32 sum of n terms by n u of their absolute values at most."""
+    d, ffn, E, dt = 64, 192, len(counts), torch.bfloat16
+    off = [0]
+    for n in counts:
+        off.append(off[-1] + n)
+    T = off[-1] + behind
+    cfg = M.MoEConfig(T=T, d=d, ffn=ffn, E=E, k=1, act="gelu_bias", capacity_factor=0.0)
+    p, q, cdf, pdf = tail_case(ffn, dt)
+    w2 = rand((E, ffn, d), 1.0, dt, 3)
+    x, dy = torch.zeros(T, d, dtype=dt), torch.zeros(T, d, dtype=dt)
+    dy[:, 9] = rand((T,), 1.0, dt, 4)
+    x[off[-1]:], dy[off[-1]:] = math.nan, math.nan
+    w = {"w1": torch.zeros(E, d, ffn, dtype=dt), "b1": p.expand(E, ffn).contiguous(), "w2": w2,
+         "b2": torch.zeros(E, d, dtype=dt)}
+    base = rand((E, ffn), 0.5, torch.float32, 5)
+    grads = {"b1": base.cuda() if accumulate else torch.full((E, ffn), math.nan, device="cuda")}
+    ws = M.Workspace(None, nbytes=M.moe_expert_ffn_backward_workspace_size(cfg))
+    wd = {n: v.cuda() for n, v in w.items()}
+    M.moe_expert_ffn_backward(cfg, wd, x.cuda(), torch.tensor(off, dtype=torch.int32).cuda(), dy.cuda(), grads, ws,
+                              accumulate=accumulate)
+    assert M.moe_check_device_status(ws)[0] == M.MOE_OK
+    got, rel = grads["b1"].double().cpu(), (3 * q * q + 120) * U
+    for e, n in enumerate(counts):
+        dh = dy[off[e]:off[e + 1], 9:10].double() * w2[e, :, 9].double()[None]
+        b0 = base[e].double() if accumulate else torch.zeros(ffn, dtype=torch.float64)
+        ref, mag = (dh * (cdf + q * pdf)).sum(0) + b0, (dh.abs() * (cdf + (q * pdf).abs())).sum(0)
+        err, tol = (got[e] - ref).abs(), (rel + (n + 2) * U) * mag + 2 * U * (ref.abs() + b0.abs()) + 1e-37
+        assert (err <= tol).all(), (e, float((err / tol).max()))
+
+
+def test_b1_gradient_with_offsets_that_are_refused():
+    """The slabs of the experts that are taken stay apart whatever the others' offsets say."""
+    d, ffn, rows, off = 64, 128, 900, [300, 333, 0, 320, 320, 900]
+    E, dt = len(off) - 1, torch.bfloat16
+    cfg = M.MoEConfig(T=rows, d=d, ffn=ffn, E=E, k=1, act="gelu_bias", capacity_factor=0.0)
+    w = {"w1": rand((E, d, ffn), 0.1, dt, 1), "b1": rand((E, ffn), 0.1, dt, 2), "w2": rand((E, ffn, d), 0.1, dt, 3),
+         "b2": rand((E, d), 0.1, dt, 4)}
+    x, dy = rand((rows, d), 1.0, dt, 5).cuda(), rand((rows, d), 0.5, dt, 6).cuda()
+    ws = M.Workspace(None, nbytes=M.moe_expert_ffn_backward_workspace_size(cfg))
+    wd = {n: v.cuda() for n, v in w.items()}
+
+    def grads(o):
+        g = {"b1": torch.empty(E, ffn, device="cuda"), "w1": torch.empty(E, d, ffn, device="cuda")}
+        M.moe_expert_ffn_backward(cfg, wd, x, torch.tensor(o, dtype=torch.int32).cuda(), dy, g, ws)
+        return g, M.moe_check_device_status(ws)[0]
+
+    bad, status = grads(off)
+    assert status == M.MOE_ERR_RANGE
+    taken = accepted(off, rows)
+    for e, (a, n) in enumerate(taken):              # each expert by itself, the others empty
+        alone, status = grads([a] * (e + 1) + [a + n] * (E - e))
+        assert status == M.MOE_OK
+        for name in alone:
+            assert torch.equal(alone[name][e], bad[name][e]), (e, name)
