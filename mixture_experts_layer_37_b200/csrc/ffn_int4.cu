@@ -33,9 +33,9 @@
 // TN = 16 for batches of few rows per expert, 64 (SwiGLU, or groups of 32: 32)
 // for more: the host chooses by the mean.  Every wait is bounded in time, as in the other kernels.
 //
-// Measured: 128 rows over 64 experts of 2048 x 2048, groups of 64, 36 to 39 us, where the codes and scales take 20 at
+// Measured: 128 rows over 64 experts of 2048 x 2048, groups of 64, 35 to 39 us, where the codes and scales take 20 at
 // the memory's rate (without the widening 32: the rest is the hand-over and 7 rounds of tiles for 6.2); 500 rows over
-// 8 experts of 4096 x 4096, groups of 128, 45 us (12): an expert of more than 64 rows takes its codes again.  (Tiles of
+// 8 experts of 4096 x 4096, groups of 128, 44 us, 33 if even (12): an expert of more than 64 rows takes its codes again.  (Tiles of
 // 128 tokens fit tensor memory for groups of 128 but leave two stages, fewer than the waits below need; 54 us was
 // measured so, which settles nothing.)
 #include <math.h>
@@ -87,9 +87,9 @@ struct I4Smem {
     // for tell that use from the one before.
     static_assert(kABufs % kGroupsOfWarps == 0, "each buffer belongs to one group of warps");
     static constexpr int kWidenWarps = 4 * kGroupsOfWarps;
-    // Four for each kTokens of the tile's tokens.  Four for all 64 (500 rows, 8 experts of 4096 x 4096: 47 us against
-    // 45; 1024 rows of 2048 x 2048, groups of 64: 32 against 27; SwiGLU FFN of 512 tokens, 16 experts of 2048 x 2048:
-    // 118 against 98) held the products up.  Four groups of widening warps instead of two: 46, 29 and 99 us.
+    // Four for each kTokens of the tile's tokens.  Four for all 64 held the products up (500 rows over 8 even experts
+    // of 4096 x 4096, groups of 128: 34.7 us against 33.0; 1024 rows of 2048 x 2048, groups of 64: 24.7 against 21.6;
+    // SwiGLU FFN of 512 tokens, 16 experts of 2048 x 2048: 61 against 56).
     static constexpr int kScaleWarps = TN == 16 ? 4 : 8;
     static constexpr int kTokens = TN / (kScaleWarps / 4);
     static constexpr int kThreads = 32 * (2 + kWidenWarps + kScaleWarps);

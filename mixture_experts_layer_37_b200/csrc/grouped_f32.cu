@@ -9,8 +9,11 @@
 // while the current ones are used; the FMAs run two at a time (f32x2, each
 // rounded as a scalar fmaf).  Every output is one sum in ascending order of
 // the contraction.  Rows and columns outside the expert are never read.
-// Bound by FMA issue: GW of 2048 rows, 8 experts of 1024 x 1024, 101 to 104 us
-// (42 TFLOP/s; 57 us at a nominal 75).
+// Measured at 2048 rows, 8 experts of 1024 x 1024 (57 us at a nominal 75
+// TFLOP/s): GW 102 to 107 us (42 TFLOP/s), the FMA pipe busy 67 % of a CTA's life
+// and 57 % of the kernel's (1.7 rounds of resident CTAs), and waiting for it the
+// largest stall; FWD 123 and GX 132 us, 52 and 50 % (47 and 44), behind loads from
+// memory and shared memory (its wavefronts 68 %).
 #include <math.h>
 
 #include "grouped.h"

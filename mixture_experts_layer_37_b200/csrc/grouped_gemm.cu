@@ -20,13 +20,13 @@
 // memory for each MMA of 128 clocks and receives as much by TMA, 24 KB where
 // the memory moves 16; a pair moves 8 KB + 8 KB per SM for the same work.
 // Measured alone the change gave 126 -> 121 us at 8192 x 2048 x 4096; elected
-// issuers then 115 -> 106 us, and 1525 -> 1366 us (1.61 PFLOP/s) at 65536 rows
-// of 4096 x 4096.  Now 105 us (1.31 PFLOP/s, of 83 us at the tensor cores'
-// peak); tensor pipe busy 76 % of it; fp32 GW that adds to 268 MB of
-// gradients, same sizes: 165 us (98 us at the memory's rate, 139 without adding).
-// There neither memory (44 %) nor the tensor pipe (42 %) is full: a tile's sums
-// pass registers and slabs in turn.  Fetching the next tile's old values into L2
-// ahead changed nothing sure (169 -> 174 us, with uneven experts 170 -> 168).
+// issuers in place of lane 0 give 101 -> 93 us there and 1440 -> 1370 us (1.61
+// PFLOP/s) at 65536 rows of 4096 x 4096 (even experts, in a graph).  With uneven
+// experts 107 us (of 83 us at the tensor cores' peak), tensor pipe busy 76 % of it;
+// fp32 GW that adds to 268 MB of gradients, same sizes: 157 us (98 us at the memory's
+// rate, 138 without adding).  There neither memory (47 %) nor the tensor pipe (46 %)
+// is full: a tile's sums pass registers and slabs in turn.  Runs of a few milliseconds
+// meet the power cap: 16384 x 4096 x 4096 GX takes 482 us at first, 560 in a long row.
 // What differs between the three forms is which operand is contiguous along
 // the contraction:
 //   FWD  A = x rows, contraction-major; B = W[e], output-major (two boxes

@@ -1086,7 +1086,7 @@ cudaError_t grouped_gx(const GroupedArgs& a, bool bf16, cudaStream_t s) {
 // sum each expert's rows in parts, joined in a fixed order.  The parts of dW:
 // as many as fill the device, none shorter than where a part's own start and
 // the join cost more than they save (bf16: 512 rows; one expert of 8071 rows,
-// 80 x 312: 46 us in one part, 15 us in these; f32: 128 rows).  Of db: 1024 rows a part.
+// 80 x 312, fp32 gradients: 69 us in one part, 21 in these; f32: 128 rows).  Of db: 1024 rows a part.
 constexpr int kPlanSms = 148;
 int gw_split(int64_t rows, int E, int K, int N, bool bf16) {
     const int64_t per = rows / E, least = bf16 ? 512 : 128;
