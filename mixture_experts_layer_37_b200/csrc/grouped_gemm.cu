@@ -89,7 +89,7 @@ enum { EPI_BF16 = 0, EPI_F32 = 1, EPI_SWIGLU_GRAD = 2, EPI_GELU_GRAD = 3 };
 template <int EPI>
 struct Smem {
     static constexpr int kSlabs = EPI != EPI_F32 ? 1 : 2;
-    static_assert(kSlabs <= 2, "an accumulating tile refills its slabs two at a time");
+    static_assert(EPI != EPI_F32 || kSlabs == 2, "an accumulating tile refills its slabs two at a time");
     static constexpr int kStages = EPI != EPI_F32 ? 6 : 5;
     static constexpr int kSlabOff = kStages * kStageBytes;
     static constexpr int kBarOff = kSlabOff + kEpiWarps * kSlabs * kSlabBytes;
@@ -662,11 +662,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
                     bool in = true;
 #pragma unroll
                     for (int c = 0; c < 128; c += 32) {
-                        if (c >= ncols || col0 + c >= p.N || !in) break;
+                        if (c >= ncols || col0 + c >= p.N) break;
                         const int s = c / 32 % S::kSlabs;
                         uint8_t* slab = slabs + s * kSlabBytes;
                         in = __all_sync(0xffffffffu, mbar_wait_bounded(&old[s], (old_par >> s) & 1u, tmo));
                         old_par ^= 1u << s;
+                        if (!in) {
+                            // the load into the other slab, issued with this one, lands before the CTA leaves
+                            if (s == 0 && c + 32 < ncols && col0 + c + 32 < p.N)
+                                mbar_wait_bounded(&old[1], (old_par >> 1) & 1u, tmo);
+                            break;
+                        }
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             float4* v = reinterpret_cast<float4*>(slab_piece(slab, lane, j));
@@ -676,7 +682,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsG, 1)
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0 && in) {
+                        if (lane == 0) {
                             tma_store<true>(&tmO, slab, col0 + c, row, t.e);
                             if (s == S::kSlabs - 1) {
                                 // the next columns into the slabs, each once its store has read it
